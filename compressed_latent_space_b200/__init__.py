@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int, c_size_t, c_uint, c_void_p
+from ctypes import POINTER, c_float, c_int, c_longlong, c_size_t, c_uint, c_void_p
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libcca.so")
@@ -24,6 +24,7 @@ CCA_ERR_ALIGNMENT = -5
 CCA_ERR_CUDA = -6
 CCA_ERR_DEVICE = -7
 CCA_ERR_RANGE = -8
+CCA_ERR_PAGE = -9
 CCA_QK_MEAN, CCA_VALUE_SHIFT, CCA_QK_NORM, CCA_ROPE = 1, 2, 4, 8
 CCA_DEFAULT_FLAGS = 15
 CCA_NO_CONV = 16
@@ -51,6 +52,18 @@ class cca_cache_t(ctypes.Structure):
     _fields_ = [("k", c_void_p), ("v", c_void_p), ("conv_state", c_void_p),
                 ("vshift_state", c_void_p), ("lengths", c_void_p), ("status", c_void_p),
                 ("batch", c_int), ("max_seq", c_int)]
+
+
+class cca_paged_cache_t(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("scales", c_void_p), ("page_table", c_void_p),
+                ("lengths", c_void_p), ("status", c_void_p), ("batch", c_int), ("max_pages", c_int),
+                ("n_pages", c_int), ("page_size", c_int), ("n_kv_heads", c_int),
+                ("head_dim", c_int), ("bits", c_int), ("dtype", c_int)]
+
+
+class cca_rows_t(ctypes.Structure):
+    _fields_ = [("ptr", c_void_p), ("dtype", c_int), ("seq_stride", c_longlong),
+                ("token_stride", c_longlong), ("head_stride", c_longlong)]
 
 
 _lib = None
@@ -87,6 +100,21 @@ _SIGS = {
     "cca_backward": (c_int, [POINTER(cca_config_t), POINTER(cca_weights_t), c_void_p, c_void_p,
                              c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                              c_void_p, c_size_t, c_void_p]),
+    "cca_paged_append": (c_int, [POINTER(cca_paged_cache_t), POINTER(cca_rows_t),
+                                 POINTER(cca_rows_t), POINTER(cca_rows_t), POINTER(cca_rows_t),
+                                 c_int, c_void_p, c_int, c_float, c_void_p]),
+    "cca_paged_gather": (c_int, [POINTER(cca_paged_cache_t), POINTER(cca_rows_t),
+                                 POINTER(cca_rows_t), c_void_p, c_int, c_void_p]),
+    "cca_paged_attention_workspace_size": (c_size_t, [POINTER(cca_paged_cache_t), c_int, c_int]),
+    "cca_paged_attention": (c_int, [POINTER(cca_paged_cache_t), POINTER(cca_rows_t),
+                                    POINTER(cca_rows_t), c_int, c_void_p, c_int, c_float, c_void_p,
+                                    c_size_t, c_void_p]),
+    "cca_paged_check": (c_int, [POINTER(cca_paged_cache_t), c_void_p]),
+    "cca_decode_step_paged_workspace_size": (c_size_t, [POINTER(cca_config_t),
+                                                        POINTER(cca_paged_cache_t)]),
+    "cca_decode_step_paged": (c_int, [POINTER(cca_config_t), POINTER(cca_weights_t), c_void_p,
+                                      c_void_p, POINTER(cca_paged_cache_t), c_void_p, c_void_p,
+                                      c_void_p, c_size_t, c_void_p]),
     "cca_stage_timing": (c_int, [c_int]),
     "cca_stage_times": (c_int, [POINTER(ctypes.c_double), c_int, POINTER(c_int)]),
 }
@@ -212,6 +240,47 @@ def cca_cache_check(cache, stream=None):
     _check(load().cca_cache_check(ctypes.byref(cache), _stream(stream)))
 
 
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def cca_paged_append(cache, q, k, v, q_out, n_heads, cu_seqlens, tokens, rope_base=0.0, stream=None):
+    """cache: cca_paged_cache_t; q, k, v, q_out: cca_rows_t (q and q_out None: no queries)."""
+    _check(load().cca_paged_append(_ref(cache), _ref(q), _ref(k), _ref(v), _ref(q_out), n_heads,
+                                   _ptr(cu_seqlens), tokens, rope_base, _stream(stream)))
+
+
+def cca_paged_gather(cache, k, v, cu_seqlens, tokens, stream=None):
+    _check(load().cca_paged_gather(_ref(cache), _ref(k), _ref(v), _ptr(cu_seqlens), tokens,
+                                   _stream(stream)))
+
+
+def cca_paged_attention_workspace_size(cache, n_heads: int, tokens: int) -> int:
+    return load().cca_paged_attention_workspace_size(_ref(cache), n_heads, tokens)
+
+
+def cca_paged_attention(cache, q, o, n_heads, cu_seqlens, tokens, scale, workspace, stream=None):
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().cca_paged_attention(_ref(cache), _ref(q), _ref(o), n_heads, _ptr(cu_seqlens),
+                                      tokens, scale, _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def cca_paged_check(cache, stream=None):
+    _check(load().cca_paged_check(_ref(cache), _stream(stream)))
+
+
+def cca_decode_step_paged_workspace_size(cfg, cache) -> int:
+    return load().cca_decode_step_paged_workspace_size(ctypes.byref(cfg), _ref(cache))
+
+
+def cca_decode_step_paged(cfg, weights, x, y, cache, conv_state, vshift_state, workspace=None,
+                          stream=None):
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().cca_decode_step_paged(ctypes.byref(cfg), ctypes.byref(weights), _ptr(x), _ptr(y),
+                                        _ref(cache), _ptr(conv_state), _ptr(vshift_state),
+                                        _ptr(workspace), ws_bytes, _stream(stream)))
+
+
 def cca_gemm_t(out_dtype, A, B, C, M, N, K, a_trans, b_trans, status=None, stream=None):
     _check(load().cca_gemm_t(out_dtype, _ptr(A), _ptr(B), _ptr(C), M, N, K, 1 if a_trans else 0,
                              1 if b_trans else 0, _ptr(status), _stream(stream)))
@@ -267,4 +336,5 @@ def cca_stage_times(n: int = 16):
     return [ms[i] for i in range(min(slots, n))], calls.value
 
 
+from .paged import PagedCache  # noqa: E402,F401
 from .layer import CCALayer  # noqa: E402,F401

@@ -14,6 +14,7 @@
 #include "cca_stages.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "paged.h"
 
 namespace {
 
@@ -667,6 +668,80 @@ CCA_API int cca_decode_step(const cca_config_t *cfg, const cca_weights_t *w, con
   rec.mark();
   cudaError_t e = cca::decode_step(d, a, static_cast<cudaStream_t>(stream), rec.marker());
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
+  return ok();
+}
+
+}  // extern "C"
+
+namespace {
+// The layer's shape and its paged cache, checked against each other.
+int check_paged_step(const cca_config_t *cfg, const cca_paged_cache_t *cache, cca::Dims &d,
+                     cca::PagedArgs &pa) {
+  int rc = make_dims(cfg, d);
+  if (rc) return rc;
+  if ((rc = check_decode_shape(d))) return rc;
+  if (!d.bf16) return fail(CCA_ERR_UNSUPPORTED, "the paged decode step runs bfloat16 layers");
+  if ((rc = cca::check_paged_cache(cache, pa))) return rc;
+  if (pa.Hkv != d.Hkv || pa.D != d.DL)
+    return fail(CCA_ERR_INVALID_ARG, "pages of %d heads of %d, the layer has %d of %d", pa.Hkv, pa.D, d.Hkv, d.DL);
+  if (pa.bits == 16 && !pa.page_f16)
+    return fail(CCA_ERR_INVALID_ARG, "a layer's 16-bit pages are CCA_F16, as its latents");
+  d.B = pa.B;
+  pa.H = d.H;
+  pa.tokens = pa.B;
+  pa.len_add = 1;
+  pa.q.dtype = CCA_F16;
+  if (cca::paged_attention_units(pa) >= (1LL << 31))
+    return fail(CCA_ERR_UNSUPPORTED, "the pages' capacity is too large for one step");
+  return CCA_OK;
+}
+}  // namespace
+
+extern "C" {
+
+CCA_API size_t cca_decode_step_paged_workspace_size(const cca_config_t *cfg,
+                                                    const cca_paged_cache_t *cache) {
+  cca::Dims d;
+  cca::PagedArgs pa;
+  if (check_paged_step(cfg, cache, d, pa)) return 0;
+  return cca::paged_step_workspace(d, pa);
+}
+
+CCA_API int cca_decode_step_paged(const cca_config_t *cfg, const cca_weights_t *w, const void *x,
+                                  void *y, const cca_paged_cache_t *cache, void *conv_state,
+                                  void *vshift_state, void *workspace, size_t ws_bytes,
+                                  void *stream) {
+  cca::Dims d;
+  cca::PagedArgs pa;
+  int rc = check_paged_step(cfg, cache, d, pa);
+  if (rc) return rc;
+  if (!w || !w->w_qkv || !w->w_o || !w->conv_seq || !w->conv_chan)
+    return fail(CCA_ERR_INVALID_ARG, "weights (or one of their pointers) NULL");
+  if (!x || !y) return fail(CCA_ERR_INVALID_ARG, "x or y NULL");
+  if (!vshift_state || (d.KC > 1 && !conv_state))
+    return fail(CCA_ERR_INVALID_ARG, "conv_state or vshift_state NULL");
+  if (!aligned16(x) || !aligned16(y) || !aligned16(w->w_qkv) || !aligned16(w->w_o) ||
+      !aligned16(workspace) || !aligned16(conv_state) || !aligned16(vshift_state))
+    return fail(CCA_ERR_ALIGNMENT, "x, y, weights, states and workspace must be 16-byte aligned");
+  const size_t need = cca::paged_step_workspace(d, pa);
+  if (!workspace || ws_bytes < need)
+    return fail(CCA_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? ws_bytes : 0, need);
+  if (injected_launch_failure()) return fail(CCA_ERR_CUDA, "injected launch failure");
+  cca::DecodeArgs a{};
+  a.x = x;
+  a.w_qkv = w->w_qkv;
+  a.w_o = w->w_o;
+  a.conv_seq = w->conv_seq;
+  a.conv_chan = w->conv_chan;
+  a.y = y;
+  a.conv_state = static_cast<float *>(conv_state);
+  a.vshift_state = static_cast<float *>(vshift_state);
+  a.lengths = cache->lengths;
+  a.status = cache->status;
+  CallRecorder rec(static_cast<cudaStream_t>(stream));
+  rec.mark();
+  const cudaError_t e = cca::decode_step_paged(d, a, pa, workspace, static_cast<cudaStream_t>(stream), rec.marker());
+  if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
   return ok();
 }
 

@@ -16,7 +16,9 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "cca.h"
 #include "kernels.h"
+#include "paged.h"
 
 namespace cca {
 namespace {
@@ -181,8 +183,18 @@ struct D2Params {
   int B, H, Hkv, G, DL, NQ, NKV, NQKV, KC, VS0, max_seq;
   unsigned flags;
   float eps;
+  bool one_row = false;    // float32 only: k_cache / v_cache hold the new row alone, [B, Hkv, d~]
   double theta[32];        // RoPE frequencies base^(-2i/d~), i < d~/2, computed on the host
 };
+
+// Where the new token's row of (sequence b, group g) goes in k_cache / v_cache, in rows.
+template <typename T>
+__device__ __forceinline__ size_t d2_row(const D2Params<T> &p, int g, int b, int L) {
+  const size_t bg = static_cast<size_t>(b) * p.Hkv + g;
+  if constexpr (sizeof(T) == 4)
+    if (p.one_row) return bg;
+  return bg * p.max_seq + L;
+}
 
 // D2 keeps the group's channel filters transposed in shared memory, wt[j][o] = the weight of
 // input j for output channel o (o over the G q heads and the k head, d~ each), rows padded to
@@ -416,7 +428,7 @@ __device__ __forceinline__ void d2_compute(const D2Params<T> &p, int g, int b, i
       q[hh * DL + ip] = x1;
       q[hh * DL + ip + HALF] = x2;
     } else {
-      auto *kd = p.k_cache + ((static_cast<size_t>(b) * p.Hkv + g) * p.max_seq + L) * DL;
+      auto *kd = p.k_cache + d2_row(p, g, b, L) * DL;
       check_latent<TL>(x1, p.status);
       check_latent<TL>(x2, p.status);
       const TL k1 = from_f32<TL>(x1), k2 = from_f32<TL>(x2);
@@ -437,7 +449,7 @@ __device__ __forceinline__ void d2_compute(const D2Params<T> &p, int g, int b, i
     const float val = ((p.flags & F_VALUE_SHIFT) && shifted) ? m.vsh[c] : m.pn[QKC + c];
     check_latent<TL>(val, p.status);
     const TL vv = from_f32<TL>(val);
-    p.v_cache[((static_cast<size_t>(b) * p.Hkv + g) * p.max_seq + L) * DL + c] = vv;
+    p.v_cache[d2_row(p, g, b, L) * DL + c] = vv;
     if (kv_keep) kv_keep[DL + c] = to_f32(vv);
   }
   // state advance (thread c rewrites only channel c's state, which it alone read)
@@ -1502,6 +1514,41 @@ static cudaError_t launch_decode_attn(const Dims &d, const DecodeArgs &a, float 
 }
 
 template <typename T>
+static void fill_d2(const Dims &d, const DecodeArgs &a, D2Params<T> &p2) {
+  using TL = typename LatentType<T>::type;
+  p2.conv_seq = a.conv_seq;
+  p2.conv_chan = a.conv_chan;
+  p2.k_cache = static_cast<TL *>(a.k_cache);
+  p2.v_cache = static_cast<TL *>(a.v_cache);
+  p2.conv_state = a.conv_state;
+  p2.vshift_state = a.vshift_state;
+  p2.lengths = a.lengths;
+  p2.status = a.status;
+  p2.q_new = a.q_new;
+  p2.B = d.B; p2.H = d.H; p2.Hkv = d.Hkv; p2.G = d.G; p2.DL = d.DL;
+  p2.NQ = d.NQ; p2.NKV = d.NKV; p2.NQKV = d.NQKV; p2.KC = d.KC; p2.VS0 = d.VS0;
+  p2.max_seq = a.max_seq;
+  p2.flags = d.flags;
+  p2.eps = d.eps;
+  for (int i = 0; i < d.DL / 2; ++i)
+    p2.theta[i] = pow(static_cast<double>(d.rope_base), -2.0 * i / d.DL);
+}
+
+template <typename T>
+static cudaError_t launch_d2(const Dims &d, const D2Params<T> &p2, cudaStream_t st) {
+  const size_t sm2 = d2_smem_floats(d.G, d.DL, d.KC) * 4;
+  auto d2 = d.DL == 16 ? decode_stencil_kernel<T, 16>
+                       : (d.DL == 32 ? decode_stencil_kernel<T, 32> : decode_stencil_kernel<T, 64>);
+  if (sm2 > 48 * 1024) {
+    const cudaError_t e = d.DL == 16 ? ensure_dyn_smem<decode_stencil_kernel<T, 16>>(sm2)
+                                     : (d.DL == 32 ? ensure_dyn_smem<decode_stencil_kernel<T, 32>>(sm2)
+                                                   : ensure_dyn_smem<decode_stencil_kernel<T, 64>>(sm2));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(d2, dim3(d.Hkv, d.B), dim3(256), sm2, st, p2);
+}
+
+template <typename T>
 static cudaError_t decode_typed(const Dims &d, const DecodeArgs &a, cudaStream_t st,
                                 const StageMarker &mark) {
   cudaError_t e;
@@ -1522,34 +1569,10 @@ static cudaError_t decode_typed(const Dims &d, const DecodeArgs &a, cudaStream_t
   D2Params<T> p2;
   p2.p_part = a.p_part;
   p2.ksplit = sizeof(T) == 2 ? a.ksplit : 1;
-  p2.conv_seq = a.conv_seq;
-  p2.conv_chan = a.conv_chan;
-  p2.k_cache = static_cast<TL *>(a.k_cache);
-  p2.v_cache = static_cast<TL *>(a.v_cache);
-  p2.conv_state = a.conv_state;
-  p2.vshift_state = a.vshift_state;
-  p2.lengths = a.lengths;
-  p2.status = a.status;
-  p2.q_new = a.q_new;
-  p2.B = d.B; p2.H = d.H; p2.Hkv = d.Hkv; p2.G = d.G; p2.DL = d.DL;
-  p2.NQ = d.NQ; p2.NKV = d.NKV; p2.NQKV = d.NQKV; p2.KC = d.KC; p2.VS0 = d.VS0;
-  p2.max_seq = a.max_seq;
-  p2.flags = d.flags;
-  p2.eps = d.eps;
-  for (int i = 0; i < d.DL / 2; ++i)
-    p2.theta[i] = pow(static_cast<double>(d.rope_base), -2.0 * i / d.DL);
+  fill_d2(d, a, p2);
   const bool fused = decode_fused(d, a.max_seq);
   if (!fused) {
-    const size_t sm2 = d2_smem_floats(d.G, d.DL, d.KC) * 4;
-    auto d2 = d.DL == 16 ? decode_stencil_kernel<T, 16>
-                         : (d.DL == 32 ? decode_stencil_kernel<T, 32> : decode_stencil_kernel<T, 64>);
-    if (sm2 > 48 * 1024) {
-      e = d.DL == 16 ? ensure_dyn_smem<decode_stencil_kernel<T, 16>>(sm2)
-                     : (d.DL == 32 ? ensure_dyn_smem<decode_stencil_kernel<T, 32>>(sm2)
-                                   : ensure_dyn_smem<decode_stencil_kernel<T, 64>>(sm2));
-      if (e != cudaSuccess) return e;
-    }
-    if ((e = launch_pdl(d2, dim3(d.Hkv, d.B), dim3(256), sm2, st, p2)) != cudaSuccess) return e;
+    if ((e = launch_d2(d, p2, st)) != cudaSuccess) return e;
     mark();
   }
   // D3 (with D2 inside when fused)
@@ -1605,6 +1628,89 @@ cudaError_t decode_step(const Dims &d, const DecodeArgs &a, cudaStream_t st,
                         const StageMarker &mark) {
   if (d.B == 0) return cudaSuccess;
   return d.bf16 ? decode_typed<__nv_bfloat16>(d, a, st, mark) : decode_typed<float>(d, a, st, mark);
+}
+
+// ------------------------------------------------------------------ the step over a paged cache
+// Projection and stencil as above, the stencil in float32 and without the rotation, which the
+// append applies to q and k on their way (so k is rounded once, into its page); then the paged
+// attention, whose output leaves in the up-projection's two bfloat16 terms.  At 64 sequences of
+// 8k tokens, d~ = 32, 4-bit pages, the step's kernels are five and the merge.
+namespace {
+struct PagedStepLayout {
+  size_t p_part, q, qr, k, v, o, attn, total;
+};
+
+PagedStepLayout paged_step_layout(const Dims &d, const PagedArgs &pa) {
+  PagedStepLayout L;
+  size_t off = 0;
+  auto take = [&](size_t bytes) { const size_t at = off; off += align256(bytes); return at; };
+  const size_t B = d.B;
+  L.p_part = take(static_cast<size_t>(decode_ksplit(d)) * B * d.NQKV * 4);
+  L.q = take(B * d.NQ * 4);
+  L.qr = take(B * d.NQ * 2);
+  L.k = take(B * d.NKV * 4);
+  L.v = take(B * d.NKV * 4);
+  L.o = take(B * d.NQ * 4);
+  L.attn = take(paged_attention_workspace(pa));
+  L.total = off;
+  return L;
+}
+}  // namespace
+
+size_t paged_step_workspace(const Dims &d, const PagedArgs &pa) { return paged_step_layout(d, pa).total; }
+
+cudaError_t decode_step_paged(const Dims &d, DecodeArgs a, PagedArgs pa, void *workspace,
+                              cudaStream_t st, const StageMarker &mark) {
+  const PagedStepLayout L = paged_step_layout(d, pa);
+  char *ws = static_cast<char *>(workspace);
+  a.p_part = reinterpret_cast<float *>(ws + L.p_part);
+  a.ksplit = decode_ksplit(d);
+  cudaError_t e = launch_skinny<true, false, 8, kQkvCols>(
+      a.ksplit, static_cast<const __nv_bfloat16 *>(a.x), nullptr,
+      static_cast<const __nv_bfloat16 *>(a.w_qkv), a.p_part, d.B, d.NQKV, d.E, nullptr, 0, st);
+  if (e != cudaSuccess) return e;
+  mark();
+  a.q_new = reinterpret_cast<float *>(ws + L.q);
+  a.k_cache = ws + L.k;
+  a.v_cache = ws + L.v;
+  a.max_seq = pa.max_pages << pa.page_log2;
+  D2Params<float> p2;
+  fill_d2(d, a, p2);
+  p2.p_part = a.p_part;
+  p2.ksplit = a.ksplit;
+  p2.one_row = true;
+  p2.flags &= ~static_cast<unsigned>(F_ROPE);
+  if ((e = launch_d2(d, p2, st)) != cudaSuccess) return e;
+  mark();
+  auto rows = [&](void *ptr, int dtype, int heads) {
+    Rows r;
+    r.ptr = ptr;
+    r.dtype = dtype;
+    r.seq = r.tok = static_cast<long long>(heads) * d.DL;
+    r.head = d.DL;
+    return r;
+  };
+  pa.q = rows(a.q_new, CCA_F32, d.H);
+  pa.qo = rows(ws + L.qr, CCA_F16, d.H);
+  pa.nk = rows(a.k_cache, CCA_F32, d.Hkv);
+  pa.nv = rows(a.v_cache, CCA_F32, d.Hkv);
+  pa.rope_base = (d.flags & F_ROPE) ? d.rope_base : 0.f;
+  if ((e = paged_append(pa, st)) != cudaSuccess) return e;
+  mark();
+  __nv_bfloat16 *o_hi = reinterpret_cast<__nv_bfloat16 *>(ws + L.o);
+  __nv_bfloat16 *o_lo = o_hi + static_cast<size_t>(d.B) * d.NQ;
+  pa.q = pa.qo;
+  pa.qo = rows(o_hi, kRowsSplit, d.H);
+  pa.o_lo = o_lo;
+  pa.scale = static_cast<float>(1.0 / sqrt(static_cast<double>(d.DL)));
+  pa.workspace = ws + L.attn;
+  if ((e = paged_attention(pa, st)) != cudaSuccess) return e;
+  mark();
+  e = launch_skinny<false, true, 8, 16>(1, o_hi, o_lo, static_cast<const __nv_bfloat16 *>(a.w_o),
+                                        a.y, d.B, d.E, d.NQ, a.lengths, a.max_seq, st);
+  if (e != cudaSuccess) return e;
+  mark();
+  return cudaSuccess;
 }
 
 }  // namespace cca

@@ -1,0 +1,91 @@
+// Device helpers shared by the paged-cache kernels (paged.cu, paged_attention.cu).
+#pragma once
+
+#include "cca.h"
+#include "common.cuh"
+#include "kernels.h"
+#include "paged.h"
+
+namespace cca {
+
+// The batch as the kernels see it: how many tokens sequence b holds (len, the call's new ones
+// included), how many of them are new (n), and where its new rows start (t0: packed row index).
+struct PagedBatch {
+  const int *lengths, *cu;
+  int B, tokens, len_add, cap;
+};
+
+struct PagedSeq {
+  int len, n, t0;
+};
+
+// A sequence whose row range leaves [0, tokens] has no new rows here, one that would pass its
+// pages' capacity holds nothing; both are reported.  len < n (a slot without a sequence has
+// len = 0) leaves the first new positions negative: they see no key and are not stored.
+__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch &p, int b, int *status) {
+  PagedSeq s;
+  if (p.cu) {
+    s.t0 = p.cu[b];
+    const int t1 = p.cu[b + 1];
+    s.n = t1 - s.t0;
+    if (s.t0 < 0 || t1 < s.t0 || t1 > p.tokens) {
+      report(status, DEV_LAYOUT);
+      s.t0 = s.n = 0;
+    }
+  } else {
+    s.n = p.tokens / p.B;
+    s.t0 = b * s.n;
+  }
+  s.len = p.lengths[b];
+  if (s.len < 0) {
+    report(status, DEV_LAYOUT);
+    s.len = 0;
+  }
+  if (s.len > p.cap - p.len_add) {
+    report(status, DEV_CACHE_FULL);
+    s.len = 0;
+  } else {
+    s.len += p.len_add;
+  }
+  return s;
+}
+
+// The page-table entry of sequence b's page `i`, -1 (reported) when it names no page.
+__device__ __forceinline__ int paged_page(const int *table, int max_pages, int n_pages, int b,
+                                          int i, int *status) {
+  const int page = table[static_cast<size_t>(b) * max_pages + i];
+  if (static_cast<unsigned>(page) >= static_cast<unsigned>(n_pages)) {
+    report(status, DEV_PAGE);
+    return -1;
+  }
+  return page;
+}
+
+__device__ __forceinline__ void store8(__half *p, const float (&v)[8]) {
+  uint4 u;
+  u.x = pack_f16x2(v[0], v[1]);
+  u.y = pack_f16x2(v[2], v[3]);
+  u.z = pack_f16x2(v[4], v[5]);
+  u.w = pack_f16x2(v[6], v[7]);
+  *reinterpret_cast<uint4 *>(p) = u;
+}
+
+// Eight consecutive elements of a CCA_* typed row (16-byte aligned) to and from floats.
+__device__ __forceinline__ void load8_as(const void *p, size_t off, int dtype, float (&o)[8]) {
+  if (dtype == CCA_F32) load8(static_cast<const float *>(p) + off, o);
+  else if (dtype == CCA_F16) load8(static_cast<const __half *>(p) + off, o);
+  else load8(static_cast<const __nv_bfloat16 *>(p) + off, o);
+}
+__device__ __forceinline__ void store8_as(void *p, size_t off, int dtype, const float (&v)[8]) {
+  if (dtype == CCA_F32) store8(static_cast<float *>(p) + off, v);
+  else if (dtype == CCA_F16) store8(static_cast<__half *>(p) + off, v);
+  else store8(static_cast<__nv_bfloat16 *>(p) + off, v);
+}
+
+__device__ __forceinline__ size_t row_offset(const Rows &r, bool packed, const PagedSeq &s, int b,
+                                             int i, int h) {
+  const long long base = packed ? static_cast<long long>(s.t0) * r.tok : static_cast<long long>(b) * r.seq;
+  return static_cast<size_t>(base + static_cast<long long>(i) * r.tok + static_cast<long long>(h) * r.head);
+}
+
+}  // namespace cca

@@ -1,0 +1,228 @@
+// The paged cache's part of the C ABI (include/cca.h): argument validation on the host and the
+// calls' launches.  No device memory is allocated here.
+#include <stdarg.h>
+#include <stdio.h>
+#include <stdlib.h>
+#include <string.h>
+
+#include <cmath>
+
+#include "cca.h"
+#include "common.cuh"
+#include "kernels.h"
+#include "paged.h"
+
+namespace {
+
+int fail(int code, const char *fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return cca::set_last_error(code, buf);
+}
+
+int ok() { return cca::set_last_error(CCA_OK, ""); }
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// The same host-side fault injection as the layer calls: CCA_FAULT_INJECT=launch.
+bool injected_launch_failure() {
+  const char *f = getenv("CCA_FAULT_INJECT");
+  return f && strcmp(f, "launch") == 0;
+}
+
+int cuda_fail(cudaError_t e, const char *what) {
+  return fail(CCA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+int check_heads(const cca::PagedArgs &a, int n_heads) {
+  if (n_heads <= 0 || n_heads % a.Hkv)
+    return fail(CCA_ERR_INVALID_ARG, "n_heads %d is not a positive multiple of n_kv_heads %d", n_heads, a.Hkv);
+  return CCA_OK;
+}
+
+int check_tokens(cca::PagedArgs &a, const int *cu, int tokens, int heads) {
+  if (tokens < 0) return fail(CCA_ERR_INVALID_ARG, "tokens must be >= 0");
+  if (!cu && tokens % a.B)
+    return fail(CCA_ERR_INVALID_ARG, "%d tokens over a batch of %d need cu_seqlens", tokens, a.B);
+  if (static_cast<long long>(tokens) * heads >= (1LL << 31) / 128)
+    return fail(CCA_ERR_UNSUPPORTED, "%d tokens of %d rows each are too many for one call", tokens, heads);
+  a.cu = cu;
+  a.tokens = tokens;
+  return CCA_OK;
+}
+
+int check_rows(const cca::PagedArgs &a, const char *name, const cca_rows_t *r, int heads,
+               bool output, cca::Rows &out) {
+  if (!r || !r->ptr) return fail(CCA_ERR_INVALID_ARG, "%s is NULL", name);
+  if (r->dtype != CCA_F32 && r->dtype != CCA_BF16 && r->dtype != CCA_F16)
+    return fail(CCA_ERR_INVALID_ARG, "%s has dtype %d", name, r->dtype);
+  const int unit = r->dtype == CCA_F32 ? 4 : 8;
+  if (!aligned16(r->ptr) || r->token_stride % unit || r->head_stride % unit || (!a.cu && r->seq_stride % unit))
+    return fail(CCA_ERR_ALIGNMENT, "%s: pointer and strides must be multiples of 16 bytes", name);
+  if (r->token_stride < 0 || r->head_stride < 0 || (!a.cu && r->seq_stride < 0))
+    return fail(CCA_ERR_INVALID_ARG, "%s has a negative stride", name);
+  const int n = a.cu ? a.tokens : a.tokens / a.B;
+  if (output && ((n > 1 && r->token_stride < a.D) || (heads > 1 && r->head_stride < a.D) ||
+                 (!a.cu && a.B > 1 && r->seq_stride < a.D)))
+    return fail(CCA_ERR_INVALID_ARG, "%s: rows of an output overlap", name);
+  out.ptr = r->ptr;
+  out.dtype = r->dtype;
+  out.seq = r->seq_stride;
+  out.tok = r->token_stride;
+  out.head = r->head_stride;
+  return CCA_OK;
+}
+
+}  // namespace
+
+namespace cca {
+// Validates a paged cache and fills the kernel-facing shape (shared with the layer's step).
+int check_paged_cache(const cca_paged_cache_t *c, PagedArgs &a) {
+  if (!c) return fail(CCA_ERR_INVALID_ARG, "paged cache is NULL");
+  if (c->batch <= 0 || c->max_pages <= 0 || c->n_pages <= 0 || c->page_size <= 0 ||
+      c->n_kv_heads <= 0 || c->head_dim <= 0)
+    return fail(CCA_ERR_INVALID_ARG, "paged cache sizes must be positive");
+  if (c->bits != 16 && c->bits != 4)
+    return fail(CCA_ERR_INVALID_ARG, "paged cache of %d bits: 16 or 4", c->bits);
+  if (c->bits == 16 && c->dtype != CCA_F16 && c->dtype != CCA_BF16)
+    return fail(CCA_ERR_INVALID_ARG, "16-bit pages are CCA_F16 or CCA_BF16 (got %d)", c->dtype);
+  if (c->head_dim != 16 && c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128)
+    return fail(CCA_ERR_UNSUPPORTED, "paged head width %d: kernels take 16, 32, 64 or 128", c->head_dim);
+  if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)))
+    return fail(CCA_ERR_UNSUPPORTED, "page_size %d: a power of two in [16, 4096]", c->page_size);
+  if (static_cast<long long>(c->max_pages) * c->page_size > (1LL << 24))
+    return fail(CCA_ERR_UNSUPPORTED, "max_pages * page_size %lld is above 2^24 tokens",
+                static_cast<long long>(c->max_pages) * c->page_size);
+  if (c->batch > 4096) return fail(CCA_ERR_UNSUPPORTED, "paged batch %d is above 4096", c->batch);
+  // n_pages * page_size is below 2^43 here, so the product with the heads stays in 64 bits
+  // once it is checked alone
+  const long long slots = static_cast<long long>(c->n_pages) * c->page_size;
+  if (slots >= (1LL << 31) || slots * c->n_kv_heads >= (1LL << 31))
+    return fail(CCA_ERR_UNSUPPORTED, "n_pages * n_kv_heads * page_size must stay below 2^31");
+  if (!c->k || !c->v || !c->page_table || !c->lengths || (c->bits == 4 && !c->scales))
+    return fail(CCA_ERR_INVALID_ARG, "paged cache has a NULL region");
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->scales))
+    return fail(CCA_ERR_ALIGNMENT, "pages and scales must be 16-byte aligned");
+  a.k = c->k;
+  a.v = c->v;
+  a.scales = c->scales;
+  a.table = c->page_table;
+  a.lengths = c->lengths;
+  a.status = c->status;
+  a.B = c->batch;
+  a.max_pages = c->max_pages;
+  a.n_pages = c->n_pages;
+  a.page_log2 = 0;
+  while ((1 << a.page_log2) < c->page_size) ++a.page_log2;
+  a.Hkv = c->n_kv_heads;
+  a.D = c->head_dim;
+  a.bits = c->bits;
+  a.page_f16 = c->dtype == CCA_F16;
+  return CCA_OK;
+}
+}  // namespace cca
+
+extern "C" {
+
+CCA_API int cca_paged_append(const cca_paged_cache_t *cache, const cca_rows_t *q,
+                             const cca_rows_t *k, const cca_rows_t *v, const cca_rows_t *q_out,
+                             int n_heads, const int *cu_seqlens, int tokens, float rope_base,
+                             void *stream) {
+  cca::PagedArgs a;
+  int rc = cca::check_paged_cache(cache, a);
+  if (rc) return rc;
+  if (!q != !q_out) return fail(CCA_ERR_INVALID_ARG, "q and q_out come together");
+  if (q && (rc = check_heads(a, n_heads))) return rc;
+  a.H = q ? n_heads : 0;
+  if ((rc = check_tokens(a, cu_seqlens, tokens, a.H + 2 * a.Hkv))) return rc;
+  if (!(rope_base == 0.f || (rope_base > 1.f && std::isfinite(rope_base))))
+    return fail(CCA_ERR_INVALID_ARG, "rope_base must be 0 (no rotation) or above 1");
+  if (tokens == 0) return ok();
+  if ((rc = check_rows(a, "k", k, a.Hkv, false, a.nk))) return rc;
+  if ((rc = check_rows(a, "v", v, a.Hkv, false, a.nv))) return rc;
+  if (q) {
+    if ((rc = check_rows(a, "q", q, n_heads, false, a.q))) return rc;
+    if ((rc = check_rows(a, "q_out", q_out, n_heads, true, a.qo))) return rc;
+  }
+  a.rope_base = rope_base;
+  if (injected_launch_failure()) return fail(CCA_ERR_CUDA, "injected launch failure");
+  const cudaError_t e = cca::paged_append(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "paged append launch");
+}
+
+CCA_API int cca_paged_gather(const cca_paged_cache_t *cache, const cca_rows_t *k,
+                             const cca_rows_t *v, const int *cu_seqlens, int tokens, void *stream) {
+  cca::PagedArgs a;
+  int rc = cca::check_paged_cache(cache, a);
+  if (rc) return rc;
+  if ((rc = check_tokens(a, cu_seqlens, tokens, 2 * a.Hkv))) return rc;
+  if (tokens == 0) return ok();
+  if ((rc = check_rows(a, "k", k, a.Hkv, true, a.nk))) return rc;
+  if ((rc = check_rows(a, "v", v, a.Hkv, true, a.nv))) return rc;
+  if (injected_launch_failure()) return fail(CCA_ERR_CUDA, "injected launch failure");
+  const cudaError_t e = cca::paged_gather(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "paged gather launch");
+}
+
+CCA_API size_t cca_paged_attention_workspace_size(const cca_paged_cache_t *cache, int n_heads,
+                                                  int tokens) {
+  cca::PagedArgs a;
+  if (cca::check_paged_cache(cache, a) || check_heads(a, n_heads) || tokens < 0) return 0;
+  a.H = n_heads;
+  a.tokens = tokens;
+  return cca::paged_attention_workspace(a);
+}
+
+CCA_API int cca_paged_attention(const cca_paged_cache_t *cache, const cca_rows_t *q,
+                                const cca_rows_t *o, int n_heads, const int *cu_seqlens,
+                                int tokens, float scale, void *workspace, size_t ws_bytes,
+                                void *stream) {
+  cca::PagedArgs a;
+  int rc = cca::check_paged_cache(cache, a);
+  if (rc) return rc;
+  if ((rc = check_heads(a, n_heads))) return rc;
+  a.H = n_heads;
+  if ((rc = check_tokens(a, cu_seqlens, tokens, n_heads))) return rc;
+  if (!std::isfinite(scale)) return fail(CCA_ERR_INVALID_ARG, "scale must be finite");
+  if (tokens == 0) return ok();
+  if ((rc = check_rows(a, "q", q, n_heads, false, a.q))) return rc;
+  if ((rc = check_rows(a, "o", o, n_heads, true, a.qo))) return rc;
+  if (a.q.dtype == CCA_F32) return fail(CCA_ERR_UNSUPPORTED, "attention queries are CCA_F16 or CCA_BF16");
+  if (a.bits == 16 && a.q.dtype != cache->dtype)
+    return fail(CCA_ERR_INVALID_ARG, "queries of 16-bit pages have the pages' dtype");
+  if (cca::paged_attention_units(a) >= (1LL << 31))
+    return fail(CCA_ERR_UNSUPPORTED, "%d tokens over pages of this capacity are too many for one call", tokens);
+  if (!aligned16(workspace)) return fail(CCA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  const size_t need = cca::paged_attention_workspace(a);
+  if (!workspace || ws_bytes < need)
+    return fail(CCA_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? ws_bytes : 0, need);
+  a.scale = scale == 0.f ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(a.D))) : scale;
+  a.workspace = workspace;
+  if (injected_launch_failure()) return fail(CCA_ERR_CUDA, "injected launch failure");
+  const cudaError_t e = cca::paged_attention(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "paged attention launch");
+}
+
+CCA_API int cca_paged_check(const cca_paged_cache_t *cache, void *stream) {
+  if (!cache) return fail(CCA_ERR_INVALID_ARG, "paged cache is NULL");
+  cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
+  if (!cache->status) return ok();
+  int s = 0;
+  if ((e = cudaMemcpy(&s, cache->status, sizeof(int), cudaMemcpyDeviceToHost)) != cudaSuccess)
+    return cuda_fail(e, "status read");
+  if (s == 0) return ok();
+  if ((e = cudaMemset(cache->status, 0, sizeof(int))) != cudaSuccess) return cuda_fail(e, "status clear");
+  switch (s) {
+    case cca::DEV_CACHE_FULL: return fail(CCA_ERR_CACHE_FULL, "a sequence is longer than its page table");
+    case cca::DEV_RANGE: return fail(CCA_ERR_RANGE, "a key or value exceeded the float16 range");
+    case cca::DEV_PAGE: return fail(CCA_ERR_PAGE, "a page-table entry names no page");
+    case cca::DEV_LAYOUT: return fail(CCA_ERR_PAGE, "cu_seqlens or lengths name no valid rows");
+    default: return fail(CCA_ERR_DEVICE, "kernel status %d", s);
+  }
+}
+
+}  // extern "C"

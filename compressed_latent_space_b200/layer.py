@@ -6,9 +6,10 @@ from __future__ import annotations
 import torch
 
 from . import (CCA_BF16, CCA_DEFAULT_FLAGS, CCA_F32, cca_backward, cca_backward_workspace_size,
-               cca_cache_alloc, cca_decode_step,
-               cca_decode_workspace_size, cca_prefill_forward, cca_prefill_workspace_size,
-               make_config, make_weights)
+               cca_cache_alloc, cca_cache_t, cca_decode_step, cca_decode_step_paged,
+               cca_decode_step_paged_workspace_size, cca_decode_workspace_size,
+               cca_prefill_forward, cca_prefill_workspace_size, make_config, make_weights)
+from .paged import PagedCache
 
 
 class Cache:
@@ -96,8 +97,47 @@ class CCALayer:
     def new_cache(self, batch: int, max_seq: int, stream=None) -> Cache:
         return Cache(self, batch, max_seq, stream)
 
-    def prefill(self, x: torch.Tensor, cache: Cache | None = None, out: torch.Tensor | None = None,
-                stream=None) -> torch.Tensor:
+    def new_paged_cache(self, batch: int, max_pages: int, page_size: int = 64, bits: int = 4,
+                        n_pages: int | None = None) -> PagedCache:
+        """A paged cache of the layer's heads (16-bit pages in float16, as its latents) with the
+        convolutions' and the value-shift's state of ``batch`` sequences.  For the layer's own
+        calls ``lengths`` holds the tokens cached so far: prefill sets it, decode advances it."""
+        c = PagedCache(batch, max_pages, page_size, self.n_kv_heads_local, self.dl, bits,
+                       torch.float16, n_pages, self.device)
+        kc1 = self.cfg.conv_kernel - 1
+        if kc1 > 0:
+            c.conv_state = torch.zeros(batch, kc1, self.n_q + self.n_kv, device=self.device)
+        # (one element at least: the state's pointer is never NULL)
+        c.vshift_state = torch.zeros(batch, max(self.n_kv - self.vshift_begin, 1), device=self.device)
+        return c
+
+    def _prefill_paged(self, x, cache: PagedCache, out, stream):
+        # the forward over dense keys and values, which go on into the pages rotated already
+        B, S, _ = x.shape
+        if B != cache.batch or S > cache.max_pages * cache.page_size:
+            raise ValueError(f"{B} x {S} tokens do not fit a paged cache of {cache.batch} x "
+                             f"{cache.max_pages * cache.page_size}")
+        if S == 0:
+            return out if out is not None else torch.empty_like(x)
+        with cache._on(stream):
+            kv = torch.empty(2, B, self.n_kv_heads_local, S, self.dl, dtype=self.latent_dtype,
+                             device=self.device)
+            dense = cca_cache_t(kv[0].data_ptr(), kv[1].data_ptr(),
+                                None if cache.conv_state is None else cache.conv_state.data_ptr(),
+                                cache.vshift_state.data_ptr(), cache.lengths.data_ptr(),
+                                cache.status.data_ptr(), B, S)
+            y = out if out is not None else torch.empty_like(x)
+            ws = torch.empty(cca_prefill_workspace_size(self.cfg, B, S), dtype=torch.uint8,
+                             device=self.device)
+            cca_prefill_forward(self.cfg, self.weights, x, B, S, y, dense, ws, stream)
+            k, v = kv.transpose(2, 3)                  # [B, S, heads, d~]
+            cache.append(k, v, stream=stream)
+        return y
+
+    def prefill(self, x: torch.Tensor, cache: Cache | PagedCache | None = None,
+                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        if isinstance(cache, PagedCache):
+            return self._prefill_paged(x, cache, out, stream)
         B, S, E = x.shape
         y = out if out is not None else torch.empty_like(x)
         ws = self.workspace(cca_prefill_workspace_size(self.cfg, B, S))
@@ -119,8 +159,16 @@ class CCALayer:
                      ws, stream)
         return dx, dw_qkv, dw_o, dconv_seq, dconv_chan
 
-    def decode(self, x: torch.Tensor, cache: Cache, out: torch.Tensor | None = None,
+    def decode(self, x: torch.Tensor, cache: Cache | PagedCache, out: torch.Tensor | None = None,
                stream=None) -> torch.Tensor:
+        if isinstance(cache, PagedCache):
+            with cache._on(stream):
+                y = out if out is not None else torch.empty_like(x)
+                ws = torch.empty(cca_decode_step_paged_workspace_size(self.cfg, cache.struct),
+                                 dtype=torch.uint8, device=self.device)
+                cca_decode_step_paged(self.cfg, self.weights, x, y, cache.struct, cache.conv_state,
+                                      cache.vshift_state, ws, stream)
+            return y
         y = out if out is not None else torch.empty_like(x)
         ws = self.workspace(cca_decode_workspace_size(self.cfg, cache.batch, cache.max_seq))
         cca_decode_step(self.cfg, self.weights, x, y, cache.struct, ws, stream)

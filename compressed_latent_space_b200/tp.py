@@ -102,6 +102,9 @@ class TPLayer:
     def new_cache(self, batch, max_seq, stream=None):
         return self.local.new_cache(batch, max_seq, stream)
 
+    def new_paged_cache(self, batch, max_pages, page_size=64, bits=4, n_pages=None):
+        return self.local.new_paged_cache(batch, max_pages, page_size, bits, n_pages)
+
     def prefill_share(self, x, cache=None, out=None, stream=None):
         """This rank's share of y, before the all-reduce."""
         return self.local.prefill(x, cache=cache, out=out, stream=stream)

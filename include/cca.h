@@ -59,7 +59,8 @@ enum {
   CCA_ERR_ALIGNMENT = -5,     /* a device pointer is not 16-byte aligned                  */
   CCA_ERR_CUDA = -6,          /* a CUDA call or kernel launch failed                      */
   CCA_ERR_DEVICE = -7,        /* a kernel reported an internal error (bounded wait ran out) */
-  CCA_ERR_RANGE = -8          /* a latent q, k or v exceeded the float16 range (16-bit layers) */
+  CCA_ERR_RANGE = -8,         /* a latent q, k or v exceeded the float16 range (16-bit layers) */
+  CCA_ERR_PAGE = -9           /* a page table names no page, or row ranges leave the tensors  */
 };
 
 /* Switches of the method's three expressivity steps and of normalisation / RoPE.
@@ -256,6 +257,133 @@ CCA_API int cca_backward(const cca_config_t *cfg, const cca_weights_t *w, const 
 /* Waits for `stream`, then returns the cache's sticky status word (CCA_OK or
  * CCA_ERR_CACHE_FULL) and clears it. */
 CCA_API int cca_cache_check(cca_cache_t *cache, void *stream);
+
+/* ------------------------------------------------------------------ paged latent cache
+ * The compressed cache in pages, for batches whose sequences differ in length and come and go:
+ * keys and values of Hkv latent heads, d~ wide, in 16 bits or in 4.  (The pages' subject is the
+ * cache that decoding streams, gist.science explainer, 1. Problem Statement; paging and 4 bits
+ * are not in the paper.)  Everything is a caller buffer:
+ *   k, v        bits 16: [n_pages, n_kv_heads, page_size, head_dim] of `dtype` (CCA_F16 or
+ *               CCA_BF16); bits 4: [n_pages, n_kv_heads, page_size, head_dim / 2] bytes, channel
+ *               2 j in the low and 2 j + 1 in the high half of byte j
+ *   scales      bits 4: [n_pages, n_kv_heads, page_size, 4] float16: key scale, key zero, value
+ *               scale, value zero of one token and head.  bits 16: NULL
+ *   page_table  [batch, max_pages] int32: page of tokens [i page_size, (i + 1) page_size) of a
+ *               sequence; entries past a sequence's tokens are not read
+ *   lengths     [batch] int32: tokens of each sequence, the new tokens of the call INCLUDED
+ *               (cca_decode_step_paged alone counts otherwise, see there).  A slot of length 0
+ *               holds no sequence: nothing is stored for it and its output rows are zero
+ *   status      int32 sticky error word, or NULL; read and cleared by cca_paged_check
+ * head_dim in {16, 32, 64, 128}; page_size a power of two in [16, 4096]; max_pages * page_size
+ * <= 2^24; batch <= 4096; n_pages * n_kv_heads * page_size < 2^31.  Two sequences may share
+ * pages they only read; rows behind a sequence's length are never read as data and may hold
+ * anything.
+ *
+ * 4 bits: a vector x (keys after the rotation) is held as zero = f16(min x), scale =
+ * f16((max x - min x) / 15) and codes n_j = clamp(round_half_even((x_j - zero) / scale), 0, 15),
+ * and reads back as scale n_j + zero.  A vector with an element that is not finite, or whose
+ * zero or scale leaves float16, reads back as NaN and records CCA_ERR_RANGE.
+ *
+ * Kernel-side errors leave the status word set and touch nothing out of range: CCA_ERR_PAGE (an
+ * entry outside [0, n_pages): its tokens are not stored and read as zeros; or cu_seqlens that
+ * leave [0, tokens], or a negative length: that sequence is taken as empty), CCA_ERR_CACHE_FULL
+ * (a length beyond max_pages * page_size: taken as empty), CCA_ERR_RANGE (a value beyond
+ * float16 stored, float16 pages and 4 bits). */
+typedef struct {
+  void *k;
+  void *v;
+  void *scales;
+  const int *page_table;
+  int *lengths;
+  int *status;
+  int batch;
+  int max_pages;
+  int n_pages;
+  int page_size;
+  int n_kv_heads;
+  int head_dim;
+  int bits;
+  int dtype;                /* cca_dtype_t of 16-bit pages: CCA_F16 or CCA_BF16 (unused at 4 bits) */
+} cca_paged_cache_t;
+
+/* Rows of a [token, head, channel] tensor of CCA_F32, CCA_BF16 or CCA_F16; channels contiguous,
+ * strides in elements, ptr and strides multiples of 16 bytes.  New tokens come
+ *   packed   (cu_seqlens given, [batch + 1] int32 on the device): token i of sequence b, head h
+ *            at ptr + (cu_seqlens[b] + i) * token_stride + h * head_stride.  Rows from
+ *            cu_seqlens[batch] on are neither read nor written.
+ *   uniform  (cu_seqlens NULL): tokens / batch new tokens each, at
+ *            ptr + b * seq_stride + i * token_stride + h * head_stride.
+ * A stride of 0 broadcasts an input; the rows of an output must not overlap. */
+typedef struct {
+  void *ptr;
+  int dtype;
+  long long seq_stride;
+  long long token_stride;
+  long long head_stride;
+} cca_rows_t;
+
+/* Appends the new tokens' keys and values to their sequences' pages: token i of n new ones goes
+ * to position lengths[b] - n + i.  With rope_base > 1 the keys, and the query rows q (n_heads
+ * heads; q and q_out NULL: none), are rotated to that position on the way (rotate-half pairing
+ * over head_dim, as the layer's RoPE: gist.science explainer, 2. Methodology, "RoPE
+ * Integration"); rope_base 0 stores them as they are.  q_out may be q.  Calling it again with
+ * the same arguments stores the same.  Positions below 0 (lengths[b] < n) are skipped, their
+ * q_out rows too.  Two tokens of one call must not fall on the same page slot (a page shared by
+ * two sequences is only read).
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CUDA. */
+CCA_API int cca_paged_append(const cca_paged_cache_t *cache, const cca_rows_t *q,
+                             const cca_rows_t *k, const cca_rows_t *v, const cca_rows_t *q_out,
+                             int n_heads, const int *cu_seqlens, int tokens, float rope_base,
+                             void *stream);
+
+/* Reads cached rows back dense: token i < min(lengths[b], room) of sequence b, where room is
+ * cu_seqlens[b + 1] - cu_seqlens[b] (packed) or tokens / batch (uniform; with the strides of a
+ * [batch, Hkv, max_seq, d~] buffer it fills cca_cache_t's k and v).  Other rows of k and v are
+ * left as they are.  Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CUDA. */
+CCA_API int cca_paged_gather(const cca_paged_cache_t *cache, const cca_rows_t *k,
+                             const cca_rows_t *v, const int *cu_seqlens, int tokens, void *stream);
+
+/* Scratch bytes needed by cca_paged_attention on the current device (0 if the cache is invalid).
+ * Nothing in it needs to start at zero; two calls that may overlap on the GPU, captured graphs
+ * included, need one each. */
+CCA_API size_t cca_paged_attention_workspace_size(const cca_paged_cache_t *cache, int n_heads,
+                                                  int tokens);
+
+/* Causal softmax attention of the new tokens over their sequences' pages, which hold them
+ * already (cca_paged_append first): the query of new token i of n sees positions
+ * 0 .. lengths[b] - n + i; query head h reads key/value head h / (n_heads / n_kv_heads), as the
+ * layer's attention (gist.science/de explainer, 2. Methodik; Extension: CCGQA).
+ *   o = softmax(scale q k^T) v       (scale 0: 1 / sqrt(head_dim))
+ * q is CCA_F16 or CCA_BF16 (at 16 bits the pages' type), o any type.  A query that sees no key
+ * (length 0, or a position below 0) gets a row of zeros.  An infinity or NaN in a cached row
+ * reaches the rows that see it, and at 16 bits may reach the other new tokens of that sequence
+ * in the same call.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, ALIGNMENT, CUDA. */
+CCA_API int cca_paged_attention(const cca_paged_cache_t *cache, const cca_rows_t *q,
+                                const cca_rows_t *o, int n_heads, const int *cu_seqlens,
+                                int tokens, float scale, void *workspace, size_t ws_bytes,
+                                void *stream);
+
+/* Waits for `stream`, then returns the cache's sticky status word (CCA_OK, CCA_ERR_CACHE_FULL,
+ * CCA_ERR_RANGE or CCA_ERR_PAGE) and clears it. */
+CCA_API int cca_paged_check(const cca_paged_cache_t *cache, void *stream);
+
+/* Scratch bytes needed by cca_decode_step_paged (0 if the config or the cache is invalid). */
+CCA_API size_t cca_decode_step_paged_workspace_size(const cca_config_t *cfg,
+                                                    const cca_paged_cache_t *cache);
+
+/* cca_decode_step over a paged cache (bfloat16 layers): projection, stencil, append (which
+ * applies the rotation), attention over the pages, up-projection.  n_kv_heads and head_dim are
+ * the layer's (a tensor-parallel rank's own heads), 16-bit pages CCA_F16 as the layer's latents.
+ * conv_state and vshift_state are cca_cache_t's, for `batch` sequences.  lengths[b] counts the
+ * tokens held BEFORE the step and is advanced by it; a sequence at max_pages * page_size is left
+ * untouched, its y row is zero and CCA_ERR_CACHE_FULL recorded.  Every slot of the batch steps:
+ * one whose sequence is shorter than its page table reaches needs that page to be its own.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, ALIGNMENT, CUDA. */
+CCA_API int cca_decode_step_paged(const cca_config_t *cfg, const cca_weights_t *w, const void *x,
+                                  void *y, const cca_paged_cache_t *cache, void *conv_state,
+                                  void *vshift_state, void *workspace, size_t ws_bytes,
+                                  void *stream);
 
 /* Text of the calling thread's last error ("" if none). */
 CCA_API const char *cca_last_error_string(void);

@@ -1,0 +1,71 @@
+"""Float64 definition of the paged cache: the 4-bit form of a vector, the cache as a dictionary
+of rows (sequence, head, position), and attention of new tokens over it.  Test infrastructure;
+shares no code with the GPU path."""
+from __future__ import annotations
+
+import numpy as np
+
+
+def quantise4(x):
+    """x [..., d] -> (codes uint8, scale, zero): min/max over the vector, both rounded to float16,
+    codes against the rounded pair.  The subtraction, division and rounding are float32's, in
+    which the form is defined (ties depend on it)."""
+    x = np.asarray(x, dtype=np.float32)
+    lo, hi = x.min(-1), x.max(-1)
+    with np.errstate(over="ignore", invalid="ignore"):
+        zero = lo.astype(np.float16)
+        scale = ((hi - lo) / np.float32(15)).astype(np.float16)
+        s, z = scale.astype(np.float32)[..., None], zero.astype(np.float32)[..., None]
+        n = np.where(s > 0, np.rint((x - z) / np.where(s > 0, s, 1)), 0)
+    bad = ~(np.isfinite(x).all(-1) & np.isfinite(zero) & np.isfinite(scale))
+    codes = np.where(bad[..., None], 0, np.clip(np.nan_to_num(n), 0, 15)).astype(np.uint8)
+    nan = np.float16(np.nan)
+    return codes, np.where(bad, nan, scale), np.where(bad, nan, zero)
+
+
+def dequantise4(codes, scale, zero):
+    return codes.astype(np.float64) * scale.astype(np.float64)[..., None] + zero.astype(np.float64)[..., None]
+
+
+def pack4(codes):
+    return (codes[..., 0::2] | (codes[..., 1::2] << 4)).astype(np.uint8)
+
+
+def unpack4(b):
+    out = np.empty(b.shape[:-1] + (2 * b.shape[-1],), np.uint8)
+    out[..., 0::2], out[..., 1::2] = b & 15, b >> 4
+    return out
+
+
+def rotate(x, pos, base):
+    """x [n, heads, d] at positions pos [n]: rotate-half pairing over d."""
+    x = np.asarray(x, dtype=np.float64)
+    half = x.shape[-1] // 2
+    ang = np.asarray(pos, dtype=np.float64)[:, None] * base ** (-np.arange(half) / half)
+    c, s = np.cos(ang)[:, None], np.sin(ang)[:, None]
+    a, b = x[..., :half], x[..., half:]
+    return np.concatenate([a * c - b * s, a * s + b * c], -1)
+
+
+def attention(q, k, v, scale, vz=None):
+    """q [n, H, d] the last n of len(k) tokens (causal), k, v [L, Hkv, d] float64 -> o [n, H, d],
+    and two sums the tests' tolerances are made of: sum_j p_j (|v_j| + |vz_j|) (vz [L, Hkv], a
+    4-bit value's zero) and the largest sum of magnitudes behind a visible score."""
+    q, k, v = (np.asarray(t, dtype=np.float64) for t in (q, k, v))
+    n, H, d = q.shape
+    L, Hkv, _ = k.shape
+    o, mass, mag = np.zeros((n, H, d)), np.zeros((n, H, d)), np.zeros((n, H))
+    for i in range(n):
+        end = L - n + i + 1
+        if end <= 0:
+            continue
+        for h in range(H):
+            g = h // (H // Hkv)
+            s = k[:end, g] @ q[i, h] * scale
+            p = np.exp(s - s.max())
+            p /= p.sum()
+            o[i, h] = p @ v[:end, g]
+            a = np.abs(v[:end, g]) if vz is None else np.abs(v[:end, g]) + np.abs(vz[:end, g])[:, None]
+            mass[i, h] = p @ a
+            mag[i, h] = (np.abs(k[:end, g]) @ np.abs(q[i, h])).max() * scale
+    return o, mass, mag
