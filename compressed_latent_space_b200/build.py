@@ -4,7 +4,9 @@
 
 Each .cu under csrc/ compiles to an object in _build/ (skipped when up to date), then
 all objects link into compressed_latent_space_b200/libcca.so with the CUDA runtime
-linked statically, so the library needs only the driver at run time.
+linked statically, so the library needs only the driver at run time.  paged_bind.cpp, the
+native marshalling of the paged-cache calls from torch tensors, becomes _paged_bind.so beside
+it (host code only; it needs torch's headers and libraries).
 """
 from __future__ import annotations
 
@@ -21,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libcca.so")
+BIND_SRC = os.path.join(CSRC, "paged_bind.cpp")
+BIND = os.path.join(PKG, "_paged_bind.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + [
@@ -59,11 +63,37 @@ def _compile(src: str, force: bool, verbose: bool) -> str:
     return obj
 
 
+def _build_bind(force: bool) -> str:
+    deps = [BIND_SRC] + _headers()
+    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= max(map(os.path.getmtime, deps)):
+        return BIND
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda]
+    for d in include_paths():
+        cmd += ["-isystem", d]
+    cmd += [BIND_SRC, "-o", BIND]
+    for d in library_paths():
+        cmd += [f"-L{d}", f"-Wl,-rpath,{d}"]
+    cmd += ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
+    return BIND
+
+
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
     with ThreadPoolExecutor(max_workers=jobs or min(8, os.cpu_count() or 4)) as ex:
+        bind = ex.submit(_build_bind, force)
         objs = list(ex.map(lambda s: _compile(s, force, verbose), srcs))
+        bind.result()
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", LIB] + objs
         r = subprocess.run(cmd, capture_output=True, text=True)

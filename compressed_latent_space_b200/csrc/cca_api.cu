@@ -691,7 +691,7 @@ int check_paged_step(const cca_config_t *cfg, const cca_paged_cache_t *cache, cc
   pa.tokens = pa.B;
   pa.len_add = 1;
   pa.q.dtype = CCA_F16;
-  if (cca::paged_attention_units(pa) >= (1LL << 31))
+  if (cca::paged_attention_units(pa) >= (1LL << 30))
     return fail(CCA_ERR_UNSUPPORTED, "the pages' capacity is too large for one step");
   return CCA_OK;
 }

@@ -96,6 +96,7 @@ int check_paged_cache(const cca_paged_cache_t *c, PagedArgs &a) {
   if (static_cast<long long>(c->max_pages) * c->page_size > (1LL << 24))
     return fail(CCA_ERR_UNSUPPORTED, "max_pages * page_size %lld is above 2^24 tokens",
                 static_cast<long long>(c->max_pages) * c->page_size);
+  if (c->n_kv_heads > 4096) return fail(CCA_ERR_UNSUPPORTED, "%d paged heads are above 4096", c->n_kv_heads);
   if (c->batch > 4096) return fail(CCA_ERR_UNSUPPORTED, "paged batch %d is above 4096", c->batch);
   // n_pages * page_size is below 2^43 here, so the product with the heads stays in 64 bits
   // once it is checked alone
@@ -193,7 +194,7 @@ CCA_API int cca_paged_attention(const cca_paged_cache_t *cache, const cca_rows_t
   if (a.q.dtype == CCA_F32) return fail(CCA_ERR_UNSUPPORTED, "attention queries are CCA_F16 or CCA_BF16");
   if (a.bits == 16 && a.q.dtype != cache->dtype)
     return fail(CCA_ERR_INVALID_ARG, "queries of 16-bit pages have the pages' dtype");
-  if (cca::paged_attention_units(a) >= (1LL << 31))
+  if (cca::paged_attention_units(a) >= (1LL << 30))
     return fail(CCA_ERR_UNSUPPORTED, "%d tokens over pages of this capacity are too many for one call", tokens);
   if (!aligned16(workspace)) return fail(CCA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
   const size_t need = cca::paged_attention_workspace(a);

@@ -2,8 +2,7 @@
 // zero per vector), for any number of new tokens per sequence and ragged lengths.
 //
 // Row r = i G + (h - g G) of sequence b and key/value head g is token i's query head h; its
-// token sits at position len - n + i and sees the keys up to there.  Rows are taken R = 8 NT at
-// a time; a work item is (sequence, head, row tile) and its units are the tiles of KT keys that
+// token sits at position len - n + i and sees the keys up to there.  Rows are taken R at a time; a work item is (sequence, head, row tile) and its units are the tiles of KT keys that
 // its last row sees.
 //
 // Mathematics, 4 bits (k_j = ks_j n_j + kz_j, v_j = vs_j u_j + vz_j with codes n, u in 0..15):
@@ -18,9 +17,14 @@
 // Both products are m16n8k16 with the keys (resp. the channels) on the 16 side and eight rows on
 // the 8 side: S^T = K Q^T and O^T = V^T P^T.  That way the usual 1 to 8 query heads of a group
 // fill the tile (16-row tiles of heads would be half empty), and both operands A come straight
-// out of row-major rows: the order of channels within a product is free as long as Q's is the
-// same, so a lane reads consecutive channels of a key; the order of keys within P V is free as
-// long as P's is the same, so a lane reads keys t, t+4, t+8, t+12 at consecutive channels.
+// out of row-major rows.  The order of channels within a product is free as long as Q's is the
+// same, and that of keys within P V as long as P's is the same:
+//   4 bits    a 16-byte piece of a row is 32 channels, to ldmatrix a row of eight 16-bit elements;
+//             plain for K (lane t: channels 8 t .. 8 t + 7 of the piece), transposed for V (lane g:
+//             channels 4 g .. 4 g + 3 of keys 2 t, 2 t + 1 in the halves of a word).  d~ = 16 has
+//             rows of 8 bytes and loads them as at 16 bits.
+//   16 bits   a lane reads consecutive channels of a key for K, and of keys t, t + 4, t + 8,
+//             t + 12 for V, whose words are paired by byte permutes.
 // S^T leaves the product with rows in lanes' columns; movmatrix turns the probabilities into the
 // second product's operand.
 //
@@ -31,11 +35,13 @@
 // bfloat16 terms (one would keep 8 bits).  q . n: the queries in float16 times a power of two
 // that brings the warp's largest to 2^14 (exact but for elements 2^28 below it).
 //
-// Split: units of all items in one line, cut into equal runs, one per warp; a warp walks its run
-// through a private ring of asynchronous copies, without any barrier.  Any mix of lengths is
-// balanced, and one long sequence uses the whole machine.  A run that covers an item writes its
-// rows; pieces of an item go to the workspace (a warp leaves at most two) and the merge kernel
-// adds them in order, so results do not depend on timing.
+// Split: the tiles of all items in one line, cut into equal runs, one per warp; a warp walks its
+// run through a private ring of asynchronous copies, without any barrier.  Any mix of lengths is
+// balanced, and one long sequence uses the whole machine.  Where there are few items (at most
+// half as many as warps) each is padded on the line to whole runs, so that no warp stops in the
+// middle to begin another item.  A run that covers an item writes its rows; pieces that meet in
+// a CTA are joined there, the rest (at most two per CTA) go through the workspace to the merge
+// kernel, always added in order, so results do not depend on timing.
 #include "paged.cuh"
 
 namespace cca {
@@ -45,6 +51,29 @@ constexpr int kWarps = 4;        // warps per CTA
 constexpr int kStages = 3;       // tiles per warp's ring, kStages - 1 in flight
 constexpr float kLazy = 8.f;     // the running maximum moves when a score passes it by this much
 
+// Division of 0 <= x < 2^31 by a divisor that the host knows (Granlund and Montgomery 1994).
+struct FastDiv {
+  uint32_t mul, shift;
+};
+FastDiv fast_div(uint32_t d) {
+  FastDiv f;
+  f.shift = 0;
+  while ((1ull << f.shift) < d) ++f.shift;
+  f.mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << f.shift) - d)) / d + 1);
+  return f;
+}
+__device__ __forceinline__ int div(int x, const FastDiv &f) {
+  return static_cast<int>((__umulhi(static_cast<uint32_t>(x), f.mul) + static_cast<uint32_t>(x)) >> f.shift);
+}
+// x / d for x >= 0 and a quotient below 2^22, rd = 1 / d: the float quotient is off by one at most.
+__device__ __forceinline__ int div(int x, int d, float rd) {
+  int q = __float2int_rz(__int2float_rn(x) * rd);
+  const int r = x - q * d;
+  if (r < 0) --q;
+  else if (r >= d) ++q;
+  return q;
+}
+
 struct AttnParams {
   PagedBatch batch;
   Rows q, o;
@@ -53,21 +82,33 @@ struct AttnParams {
   const uint2 *scales;
   const int *table;
   int *status;
-  int *pre;                      // [B + 1] units before each sequence (written by CTA 0)
-  float *part_o;                 // [2 warps][R][D]
-  float2 *part_ml;               // [2 warps][R]
+  int *plan;                     // [B + 3]: units before each sequence, run length, item padding
+  float *spill;                  // [warps][R D + 2 R]
+  float *part_o;                 // [2 CTAs][R][D]
+  float2 *part_ml;               // [2 CTAs][R]
   int max_pages, n_pages, page_log2, Hkv, G, warps;
+  FastDiv by_g, by_hkv;
+  int whole;                     // > 0: items are never split, none has more tiles than this
   float scale_log2;
 };
 
 template <int D, int BITS>
 struct Shape {
   static constexpr int ROWB = BITS == 4 ? D / 2 : 2 * D;      // bytes of a cached row
-  static constexpr int KT = (BITS == 16 && D == 128) ? 32 : 64;  // keys per tile
+  static constexpr int KTL = BITS == 16 && D == 128 ? 4 : (BITS == 16 && D == 64 ? 5 : 6);
+  static constexpr int KT = 1 << KTL;                         // keys per tile
   static constexpr int KB = KT / 16;
   static constexpr int TILE = KT * (2 * ROWB + (BITS == 4 ? 8 : 0));
   static constexpr size_t SMEM = static_cast<size_t>(kWarps) * kStages * TILE;
 };
+
+// CTAs per SM that the registers are allotted for: as many as fit without spilling.
+constexpr int ctas_by_regs(int d, int bits, int rows) {
+  if (rows == 32) return 2;
+  if (rows == 16) return d <= 32 ? 3 : 2;
+  if (d == 128) return bits == 4 ? 3 : 2;
+  return bits == 4 && d <= 32 ? 5 : (bits == 16 && d == 64 ? 3 : 4);
+}
 
 // 16-byte piece `c` of row `r` of a 16-bit tile, in pieces from the tile's start: an XOR order
 // in which both the key reads (rows g and their neighbours 4 on, consecutive pieces) and the
@@ -82,6 +123,18 @@ __device__ __forceinline__ int piece16(int r, int c) {
   else
     return (r * 2 + c) ^ (((r >> 2) & 1) << 2);
 }
+
+// The same for 4-bit rows of 16, 32 or 64 bytes, read by ldmatrix (eight rows, one piece).
+template <int D>
+__device__ __forceinline__ int piece4(int r, int c) {
+  if constexpr (D == 64) return r * 2 + (c ^ ((r >> 2) & 1));
+  else if constexpr (D == 128) return r * 4 + (c ^ ((r >> 1) & 3));
+  else return r * (D / 32) + c;
+}
+
+// Byte of key `key`'s scales and zeros in a tile's: eight bytes each, odd blocks of 16 keys with
+// their halves swapped, so that two blocks read at once lie in different banks.
+__device__ __forceinline__ uint32_t scale_at(int key) { return (key * 8) ^ (((key >> 4) & 1) << 6); }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
@@ -110,27 +163,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                : "r"(a));
   return v;
 }
-// n consecutive words (1, 2, 4 or a multiple of 4) of a lane
-template <int N>
-__device__ __forceinline__ void lds_words(uint32_t a, uint32_t *w) {
-  if constexpr (N == 1) {
-    w[0] = lds32(a);
-  } else if constexpr (N == 2) {
-    const uint2 u = lds64(a);
-    w[0] = u.x;
-    w[1] = u.y;
-  } else {
-    static_assert(N % 4 == 0, "");
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const uint4 u = lds128(a + 4 * i);
-      w[i] = u.x;
-      w[i + 1] = u.y;
-      w[i + 2] = u.z;
-      w[i + 3] = u.w;
-    }
-  }
-}
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -142,56 +174,75 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Keys tiles that rows up to (row tile rt) of a sequence see; one even where there is none, so
-// that some warp writes the rows.
-__device__ __forceinline__ int tiles_of(const PagedSeq &s, int rt, int R, int G, int kt_log2) {
-  const int last = min(s.n - 1, (rt * R + R - 1) / G);
+// Tiles of keys that the rows of row tile rt see; one even where there is none, so that some
+// warp writes the rows.
+__device__ __forceinline__ int tiles_of(const PagedSeq &s, int rt, int R, const FastDiv &by_g, int kt_log2) {
+  const int last = min(s.n - 1, div(rt * R + R - 1, by_g));
   const int keys = max(0, min(s.len, s.len - s.n + last + 1));
   return max(1, (keys + (1 << kt_log2) - 1) >> kt_log2);
 }
 __device__ __forceinline__ int row_tiles(const PagedSeq &s, int R, int G) {
   return (s.n * G + R - 1) / R;
 }
-__device__ __forceinline__ int units_per_head(const PagedSeq &s, int R, int G, int kt_log2) {
-  const int rts = row_tiles(s, R, G);
-  int u = 0;
-  for (int rt = 0; rt < rts; ++rt) u += tiles_of(s, rt, R, G, kt_log2);
-  return u;
+// Units of an item on the line.
+__device__ __forceinline__ int padded(int tiles, int pad, float rpad) {
+  return div(tiles + pad - 1, pad, rpad) * pad;
+}
+// Where row r of (sequence b, head h) goes in the output.
+__device__ __forceinline__ size_t out_offset(const AttnParams &p, const PagedSeq &s, int b, int h, int r) {
+  const int tok = div(r, p.by_g);
+  return row_offset(p.o, p.batch.cu != nullptr, s, b, tok, h * p.G + r - tok * p.G);
 }
 
-template <int D, int BITS, int NT, bool QBF16, bool PBF16>
+// RW rows per tile.  Up to 8 rows share one 8-column product; with RW = 4 or 2 the columns are
+// split among X = 8 / RW blocks of 16 keys (block x's products run against queries that are zero
+// outside columns [x RW, (x + 1) RW), so X of them add up in one accumulator without touching
+// each other), and everything done per score costs 1 / X.  Each column group keeps its own
+// running maximum and sums; finish() joins them.
+template <int D, int BITS, int RW, bool QBF16, bool PBF16>
 struct Core {
   using S = Shape<D, BITS>;
-  static constexpr int KS = D / 16, MT = D / 16, KB = S::KB;
+  static constexpr int NT = RW <= 8 ? 1 : RW / 8, X = RW < 8 ? 8 / RW : 1, GP = 8 / X;
+  static constexpr int KS = D / 16, MT = D / 16, SF = S::KB / X;   // score fragments per tile
   // tensor-core element types: the queries and 16-bit keys in the pages' type, codes in float16
   static constexpr bool BF_QK = BITS == 16 && PBF16;
+  static_assert(S::KB % X == 0 && S::KB % (D == 32 ? 2 : 1) == 0, "");
+  static constexpr bool LDSM = BITS == 4 && D >= 32;   // operands by ldmatrix, keys in their order
+  // output channels of a lane: CH pieces of N consecutive ones, piece c from channel ch0(c, g) on
+  static constexpr int CH = LDSM ? D / 32 : 1, N = LDSM ? 4 : D / 8;
+  static __device__ __forceinline__ int ch0(int c, int g) { return c * 32 + g * N; }
 
-  uint32_t qf[NT][KS][2];
+  uint32_t qf[X][NT][KS][2];
   float qz[NT][2];               // scale_log2 * sum of the row's query (4 bits)
   float ksf;                     // factor of a raw score into log2 units
   float m[NT][2], l[NT][2], z[NT][2];
   float o[MT][NT][4];
   float nrm;
+  bool first;                    // no tile yet: m is not a maximum
 
   __device__ __forceinline__ void mma_qk(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
     if constexpr (BF_QK) mma_bf16_16816(d, a, b);
     else mma_f16_16816(d, a, b);
   }
 
-  // queries of rows [r0, r0 + R) (zero past `rows`) as B fragments
-  __device__ __forceinline__ void load_q(const AttnParams &p, const PagedSeq &s, int b, int h,
-                                         int r0, int rows, int g, int t) {
-    constexpr int E = D / 4;                         // channels [t E, t E + E) of row g
-    float mxq = 0.f;
-    uint32_t w[NT][E / 2];
+  // the row of a tile that column `col` of n-tile nt belongs to
+  static __device__ __forceinline__ int row_of(int nt, int col) { return nt * 8 + col % GP; }
+
+  // a lane's E channels of a row: 8 t .. 8 t + 7 of every 32 (LDSM), else [t E, t E + E)
+  static constexpr int E = D / 4;
+  using Raw = uint32_t[NT][E / 2];
+
+  // queries of rows [r0, r0 + RW) (zero past `rows`), column g
+  static __device__ __forceinline__ void load_q(const AttnParams &p, const PagedSeq &s, int b, int h,
+                                                int r0, int rows, int g, int t, Raw &w) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = r0 + nt * 8 + g;
+      const int r = r0 + row_of(nt, g);
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) w[nt][i] = 0u;
       if (r < rows) {
-        const int tok = r / p.G, hh = h * p.G + r % p.G;
-        const size_t off = row_offset(p.q, p.batch.cu != nullptr, s, b, tok, hh) + t * E;
+        const int tok = div(r, p.by_g), hh = h * p.G + r - tok * p.G;
+        const size_t off = row_offset(p.q, p.batch.cu != nullptr, s, b, tok, hh) + t * (LDSM ? 8 : E);
         const uint32_t *src = reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.q.ptr) + off);
         if constexpr (E == 4) {
           const uint2 u = *reinterpret_cast<const uint2 *>(src);
@@ -200,7 +251,7 @@ struct Core {
         } else {
 #pragma unroll
           for (int i = 0; i < E / 2; i += 4) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(src + i);
+            const uint4 u = *reinterpret_cast<const uint4 *>(src + (LDSM ? 4 * i : i));
             w[nt][i] = u.x;
             w[nt][i + 1] = u.y;
             w[nt][i + 2] = u.z;
@@ -209,16 +260,25 @@ struct Core {
         }
       }
     }
+  }
+
+  // the same as B fragments
+  __device__ __forceinline__ void set_q(const AttnParams &p, const Raw &w, int g, int t) {
+    auto put = [&](int nt, int ks, int i, uint32_t v) {
+#pragma unroll
+      for (int x = 0; x < X; ++x) qf[x][nt][ks][i] = X == 1 || g / GP == x ? v : 0u;
+    };
     if constexpr (BITS == 16) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          qf[nt][ks][0] = w[nt][2 * ks];
-          qf[nt][ks][1] = w[nt][2 * ks + 1];
+          put(nt, ks, 0, w[nt][2 * ks]);
+          put(nt, ks, 1, w[nt][2 * ks + 1]);
         }
       ksf = p.scale_log2;
     } else {
+      float mxq = 0.f;
       auto val = [&](int nt, int i) {
         const uint32_t x = w[nt][i >> 1];
         const uint32_t hx = (i & 1) ? x >> 16 : x & 0xffffu;
@@ -245,21 +305,20 @@ struct Core {
       // 2^(14 - floor(log2 mxq)), the exponent kept within what the inverse below can hold
       int e = static_cast<int>((__float_as_uint(mxq) >> 23) & 255u) - 127;
       e = max(-100, min(100, e));
-      const float f = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+      const float f = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23), f16 = f * 0.0625f;
       ksf = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(24 - 14 + e + 127) << 23);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if constexpr (D == 16) {
-          qf[nt][0][0] = pack_f16x2(val(nt, 0) * f, val(nt, 1) * f * 0.0625f);
-          qf[nt][0][1] = pack_f16x2(val(nt, 2) * f, val(nt, 3) * f * 0.0625f);
+          put(nt, 0, 0, pack_f16x2(val(nt, 0) * f, val(nt, 1) * f16));
+          put(nt, 0, 1, pack_f16x2(val(nt, 2) * f, val(nt, 3) * f16));
         } else {
 #pragma unroll
           for (int i = 0; i < E / 8; ++i) {
-            const float f16 = f * 0.0625f;
-            qf[nt][2 * i][0] = pack_f16x2(val(nt, 8 * i) * f, val(nt, 8 * i + 4) * f);
-            qf[nt][2 * i][1] = pack_f16x2(val(nt, 8 * i + 1) * f16, val(nt, 8 * i + 5) * f16);
-            qf[nt][2 * i + 1][0] = pack_f16x2(val(nt, 8 * i + 2) * f, val(nt, 8 * i + 6) * f);
-            qf[nt][2 * i + 1][1] = pack_f16x2(val(nt, 8 * i + 3) * f16, val(nt, 8 * i + 7) * f16);
+            put(nt, 2 * i, 0, pack_f16x2(val(nt, 8 * i) * f, val(nt, 8 * i + 4) * f));
+            put(nt, 2 * i, 1, pack_f16x2(val(nt, 8 * i + 1) * f16, val(nt, 8 * i + 5) * f16));
+            put(nt, 2 * i + 1, 0, pack_f16x2(val(nt, 8 * i + 2) * f, val(nt, 8 * i + 6) * f));
+            put(nt, 2 * i + 1, 1, pack_f16x2(val(nt, 8 * i + 3) * f16, val(nt, 8 * i + 7) * f16));
           }
         }
       }
@@ -268,40 +327,78 @@ struct Core {
 
   __device__ __forceinline__ void reset() {
     nrm = __uint_as_float(227u << 23);               // 2^100: the first scale met brings it down
+    first = true;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m[nt][e] = -INFINITY;
-        l[nt][e] = z[nt][e] = 0.f;
-      }
+      for (int e = 0; e < 2; ++e) m[nt][e] = l[nt][e] = z[nt][e] = 0.f;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
   }
 
-  // A fragments of 16 keys (MMA row g = key kp, row g + 8 = key kp + 8 of the block)
+  // Words of the lane's channels of keys g and g + 8 of block `blk` (and, d~ = 32, of the next
+  // block in the second pair): LDSM
+  static constexpr int BPL = D == 32 ? 2 : 1;        // blocks per load
+  __device__ __forceinline__ void load_k4(uint32_t base, int blk, int lane, uint32_t (&w)[BPL][2][D / 32]) {
+    if constexpr (D == 32) {
+      ldsm_x4(base + (blk * 16 + lane) * 16, w[0][0][0], w[0][1][0], w[1][0][0], w[1][1][0]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < D / 32; c += 2)
+        ldsm_x4(base + piece4<D>(blk * 16 + (lane & 15), c + (lane >> 4)) * 16, w[0][0][c], w[0][1][c],
+                w[0][0][c + 1], w[0][1][c + 1]);
+    }
+  }
+  // codes to operands: n 2^-24 and n 2^-20 by turns
+  static __device__ __forceinline__ void spread_k(const uint32_t (&w)[2][D / 32], uint32_t (&a)[KS][4]) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t x = w[half][i], y = x >> 8;
+        a[2 * i][half] = x & 0x000f000fu;
+        a[2 * i][2 + half] = x & 0x00f000f0u;
+        a[2 * i + 1][half] = y & 0x000f000fu;
+        a[2 * i + 1][2 + half] = y & 0x00f000f0u;
+      }
+  }
+  // V: word [key half][piece], channels 4 g .. 4 g + 3 of a piece of keys 2 t and 2 t + 1
+  __device__ __forceinline__ void load_v4(uint32_t base, int blk, int lane, uint32_t (&w)[BPL][2][D / 32]) {
+    if constexpr (D == 32) {
+      ldsm_x4_t(base + (blk * 16 + lane) * 16, w[0][0][0], w[0][1][0], w[1][0][0], w[1][1][0]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < D / 32; c += 2)
+        ldsm_x4_t(base + piece4<D>(blk * 16 + (lane & 15), c + (lane >> 4)) * 16, w[0][0][c], w[0][1][c],
+                  w[0][0][c + 1], w[0][1][c + 1]);
+    }
+  }
+  // products 2 c and 2 c + 1 of piece c: channels 4 g (row g) and 4 g + 1 (row g + 8), then + 2, + 3
+  static __device__ __forceinline__ void spread_v(const uint32_t (&w)[2][D / 32], uint32_t (&a)[MT][4]) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        const uint32_t x = w[half][c], y = x >> 8;
+        a[2 * c][2 * half] = x & 0x000f000fu;
+        a[2 * c][2 * half + 1] = x & 0x00f000f0u;
+        a[2 * c + 1][2 * half] = y & 0x000f000fu;
+        a[2 * c + 1][2 * half + 1] = y & 0x00f000f0u;
+      }
+  }
+
+  // A fragments of 16 keys without ldmatrix (MMA row g = key kp, row g + 8 = key kp + 8)
   __device__ __forceinline__ void load_k(uint32_t base, int blk, int kp, int t, uint32_t (&a)[KS][4]) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int key = blk * 16 + kp + 8 * half;
-      if constexpr (BITS == 4 && D == 16) {
+      if constexpr (BITS == 4) {                     // d~ = 16
         uint32_t w = lds16(base + key * 8 + t * 2);
         w |= w << 16;
         a[0][half] = w & 0x00f0000fu;
         a[0][2 + half] = (w >> 8) & 0x00f0000fu;
-      } else if constexpr (BITS == 4) {
-        uint32_t w[D / 32];
-        lds_words<D / 32>(base + key * S::ROWB + t * (D / 8), w);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          a[2 * i][half] = w[i] & 0x000f000fu;
-          a[2 * i][2 + half] = w[i] & 0x00f000f0u;
-          const uint32_t u = w[i] >> 8;
-          a[2 * i + 1][half] = u & 0x000f000fu;
-          a[2 * i + 1][2 + half] = u & 0x00f000f0u;
-        }
       } else if constexpr (D == 16) {
         const uint2 u = lds64(base + piece16<D>(key, t >> 1) * 16 + (t & 1) * 8);
         a[0][half] = u.x;
@@ -319,45 +416,19 @@ struct Core {
     }
   }
 
-  // A fragments of V^T: lane g's channels [g D/8, ..), channel 2 mt in MMA row g and 2 mt + 1 in
-  // row g + 8 of product mt; keys t, t + 4, t + 8, t + 12 of the block
+  // A fragments of V^T without ldmatrix: lane g's channels [g D/8, ..), channel 2 mt in MMA row g
+  // and 2 mt + 1 in row g + 8 of product mt; keys t, t + 4, t + 8, t + 12 of the block
   __device__ __forceinline__ void load_v(uint32_t base, int blk, int g, int t, uint32_t (&a)[MT][4]) {
     const int k0 = blk * 16 + t;
-    if constexpr (BITS == 4) {
-      constexpr int W = D == 128 ? 2 : 1;
-      uint32_t w[4][W];
+    constexpr int W = D / 16;                        // words of a lane's D / 8 channels
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t at = base + (k0 + 4 * i) * S::ROWB + g * (D / 16);
-        if constexpr (D == 128) lds_words<2>(at, w[i]);
-        else if constexpr (D == 64) w[i][0] = lds32(at);
-        else if constexpr (D == 32) w[i][0] = lds16(at);
-        else w[i][0] = lds8(at);
-      }
-#pragma unroll
-      for (int pr = 0; pr < 2; ++pr) {               // key pairs (t, t+4), (t+8, t+12)
-#pragma unroll
-        for (int x = 0; x < W; ++x) {
-          const uint32_t lo = __byte_perm(w[2 * pr][x], w[2 * pr + 1][x], 0x5410);
-          a[x * 4][2 * pr] = lo & 0x000f000fu;
-          a[x * 4][2 * pr + 1] = lo & 0x00f000f0u;
-          if constexpr (D >= 32) {
-            a[x * 4 + 1][2 * pr] = (lo >> 8) & 0x000f000fu;
-            a[x * 4 + 1][2 * pr + 1] = (lo >> 8) & 0x00f000f0u;
-          }
-          if constexpr (D >= 64) {
-            const uint32_t hi = __byte_perm(w[2 * pr][x], w[2 * pr + 1][x], 0x7632);
-            a[x * 4 + 2][2 * pr] = hi & 0x000f000fu;
-            a[x * 4 + 2][2 * pr + 1] = hi & 0x00f000f0u;
-            a[x * 4 + 3][2 * pr] = (hi >> 8) & 0x000f000fu;
-            a[x * 4 + 3][2 * pr + 1] = (hi >> 8) & 0x00f000f0u;
-          }
-        }
-      }
-    } else {
-      constexpr int W = D / 16;                      // words of a lane's D / 8 channels
-#pragma unroll
-      for (int pr = 0; pr < 2; ++pr) {
+    for (int pr = 0; pr < 2; ++pr) {                 // key pairs (t, t+4), (t+8, t+12)
+      if constexpr (BITS == 4) {                     // d~ = 16
+        const uint32_t at = base + (k0 + 8 * pr) * 8 + g;
+        const uint32_t lo = lds8(at) | lds8(at + 32) << 16;
+        a[0][2 * pr] = lo & 0x000f000fu;
+        a[0][2 * pr + 1] = lo & 0x00f000f0u;
+      } else {
         uint32_t x[W], y[W];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -371,7 +442,13 @@ struct Core {
             w[1] = u.y;
           } else {
 #pragma unroll
-            for (int i = 0; i < W; i += 4) lds_words<4>(base + piece16<D>(key, g * (W / 4) + i / 4) * 16, w + i);
+            for (int i = 0; i < W; i += 4) {
+              const uint4 u = lds128(base + piece16<D>(key, g * (W / 4) + i / 4) * 16);
+              w[i] = u.x;
+              w[i + 1] = u.y;
+              w[i + 2] = u.z;
+              w[i + 3] = u.w;
+            }
           }
         }
 #pragma unroll
@@ -383,169 +460,216 @@ struct Core {
     }
   }
 
-  // One tile of KT keys from key `key0` on.  lim[nt][e]: keys that row 2 t + e of n-tile nt
-  // sees; MASK where some row does not see the whole tile.
+  // One tile of KT keys from key `key0` on.  lim[nt][e]: keys that the row of column 2 t + e of
+  // n-tile nt sees; MASK where some row does not see the whole tile.  (Rows see prefixes: one
+  // that sees nothing of a run's first tile sees nothing of the run.)
   template <bool MASK>
   __device__ __forceinline__ void tile(uint32_t kbase, uint32_t vbase, uint32_t sbase, int key0,
                                        const int (&lim)[NT][2], int len, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const int kp = (g >> 1) + 4 * (g & 1);           // the key of MMA row g within its block
-    float c[KB][NT][4];
-    float2 kzs[KB][2], vzs[KB][2];                   // (scale, zero) of the lane's keys
+    const int kp = LDSM ? g : (g >> 1) + 4 * (g & 1);   // the key of MMA row g within its block
+    const int xt = 2 * t / GP;                       // the block of a group that the lane's columns score
+    float c[SF][NT][4];
+    float2 vzs[SF][2];                               // (scale, zero) of the lane's values
+    float top = -INFINITY, vtop = 0.f;
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      uint32_t a[KS][4];
-      load_k(kbase, kb, kp, t, a);
+    for (int f = 0; f < SF; ++f)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) c[kb][nt][0] = c[kb][nt][1] = c[kb][nt][2] = c[kb][nt][3] = 0.f;
+      for (int nt = 0; nt < NT; ++nt) c[f][nt][0] = c[f][nt][1] = c[f][nt][2] = c[f][nt][3] = 0.f;
+    if constexpr (LDSM) {
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
+      for (int blk = 0; blk < S::KB; blk += BPL) {
+        uint32_t w[BPL][2][D / 32];
+        load_k4(kbase, blk, lane, w);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_qk(c[kb][nt], a[ks], qf[nt][ks]);
-      if constexpr (BITS == 4) {
+        for (int i = 0; i < BPL; ++i) {
+          uint32_t a[KS][4];
+          spread_k(w[i], a);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int key = kb * 16 + kp + 8 * e;
-          const uint2 u = lds64(sbase + key * 8);
-          kzs[kb][e] = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
-          vzs[kb][e] = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
-          kzs[kb][e].x *= ksf;
-          if (MASK && key0 + key >= len) vzs[kb][e] = make_float2(0.f, 0.f);  // no such key
+          for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_qk(c[(blk + i) / X][nt], a[ks], qf[(blk + i) % X][nt][ks]);
         }
       }
+    } else {
+#pragma unroll
+      for (int blk = 0; blk < S::KB; ++blk) {
+        uint32_t a[KS][4];
+        load_k(kbase, blk, kp, t, a);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_qk(c[blk / X][nt], a[ks], qf[blk % X][nt][ks]);
+      }
     }
-    auto score = [&](int kb, int nt, int e, float mm) {   // log2 units, less mm
-      const int half = e >> 1, col = e & 1;
-      if constexpr (BITS == 4)
-        return fmaf(c[kb][nt][e], kzs[kb][half].x, fmaf(kzs[kb][half].y, qz[nt][col], -mm));
-      else
-        return fmaf(c[kb][nt][e], ksf, -mm);
-    };
-    auto seen = [&](int kb, int nt, int e) {
-      return key0 + kb * 16 + kp + 8 * (e >> 1) < lim[nt][e & 1];
-    };
-    float top = -INFINITY;
-    float mv[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int f = 0; f < SF; ++f) {
+      const int kf = (f * X + xt) * 16 + kp;         // the lane's keys: kf, kf + 8
+      // scores in log2 units, less the running maximum
 #pragma unroll
-      for (int e = 0; e < 2; ++e) mv[nt][e] = m[nt][e];
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = score(kb, nt, e, m[nt][e & 1]);
-          if (MASK && !seen(kb, nt, e)) x = -INFINITY;
-          top = fmaxf(top, x);
+      for (int half = 0; half < 2; ++half) {
+        uint64_t ks2 = 0, kz2 = 0;
+        if constexpr (BITS == 4) {
+          const uint2 u = lds64(sbase + scale_at(kf + 8 * half));
+          const float2 kk = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
+          vzs[f][half] = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
+          if (MASK && key0 + kf + 8 * half >= len) vzs[f][half] = make_float2(0.f, 0.f);   // no such key
+          vtop = fmaxf(vtop, vzs[f][half].x);
+          const float k = kk.x * ksf;
+          ks2 = f2(k, k);
+          kz2 = f2(kk.y, kk.y);
+        } else {
+          ks2 = f2(ksf, ksf);
         }
-    bool grow = top > kLazy;
-    float vmax = 0.f;
-    if constexpr (BITS == 4) {
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) vmax = fmaxf(vmax, fmaxf(vzs[kb][0].x, vzs[kb][1].x));
-      grow = grow || vmax * nrm > 128.f;
-    }
-    if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int col = 0; col < 2; ++col) {
-          float mx = mv[nt][col];
-#pragma unroll
-          for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int e = 2 * half + col;
-              float x = score(kb, nt, e, 0.f);
-              if (MASK && !seen(kb, nt, e)) x = -INFINITY;
-              mx = fmaxf(mx, x);
-            }
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float al = mv[nt][col] == -INFINITY ? 0.f : ex2(mv[nt][col] - mx);
-          m[nt][col] = mx;
-          l[nt][col] *= al;
-          z[nt][col] *= al;
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            o[mt][nt][col] *= al;
-            o[mt][nt][2 + col] *= al;
+        for (int nt = 0; nt < NT; ++nt) {
+          uint64_t off = f2(-m[nt][0], -m[nt][1]);
+          if constexpr (BITS == 4) off = fma2(kz2, f2(qz[nt][0], qz[nt][1]), off);
+          float x0, x1;
+          unf2(fma2(f2(c[f][nt][2 * half], c[f][nt][2 * half + 1]), ks2, off), x0, x1);
+          if (MASK) {
+            if (key0 + kf + 8 * half >= lim[nt][0]) x0 = -INFINITY;
+            if (key0 + kf + 8 * half >= lim[nt][1]) x1 = -INFINITY;
           }
-        }
-      if constexpr (BITS == 4) {
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1)
-          vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
-        if (vmax * nrm > 128.f) {                    // warp-uniform: lanes of one g agree already
-          const int e = static_cast<int>((__float_as_uint(vmax) >> 23) & 255u) - 127;
-          const float nn = __uint_as_float(static_cast<uint32_t>(6 - e + 127) << 23);
-          const float f = nn / nrm;
-          nrm = nn;
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e4 = 0; e4 < 4; ++e4) o[mt][nt][e4] *= f;
+          c[f][nt][2 * half] = x0;
+          c[f][nt][2 * half + 1] = x1;
+          top = max3(top, x0, x1);
         }
       }
     }
+    if (__any_sync(0xffffffffu, first || top > kLazy || (BITS == 4 && vtop * nrm > 128.f))) raise(c, vtop);
+    uint32_t pb[SF][NT][2], pl[SF][NT][2];
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      uint32_t pb[NT][2], pl[NT][2];
-      float vn[2] = {0.f, 0.f};
-      if constexpr (BITS == 4) {
-        vn[0] = vzs[kb][0].x * nrm;
-        vn[1] = vzs[kb][1].x * nrm;
-      }
+    for (int f = 0; f < SF; ++f) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
+        uint32_t w[2], wl[2] = {0u, 0u};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool on = !MASK || seen(kb, nt, e);
-          const float pr = on ? ex2(score(kb, nt, e, m[nt][e & 1])) : 0.f;
-          l[nt][e & 1] += pr;
+        for (int half = 0; half < 2; ++half) {
+          const float x0 = c[f][nt][2 * half], x1 = c[f][nt][2 * half + 1];
+          const float p0 = ex2(x0), p1 = ex2(x1);
+          const uint64_t p2 = f2(p0, p1);
+          uint64_t acc = add2(f2(l[nt][0], l[nt][1]), p2);
+          unf2(acc, l[nt][0], l[nt][1]);
           if constexpr (BITS == 4) {
-            w[e] = on ? pr * vn[e >> 1] : 0.f;       // a masked key's scale may be anything
-            z[nt][e & 1] = on ? fmaf(pr, vzs[kb][e >> 1].y, z[nt][e & 1]) : z[nt][e & 1];
+            const float vn = vzs[f][half].x * nrm, vz = vzs[f][half].y;
+            float w0, w1, z0, z1;
+            unf2(mul2(p2, f2(vn, vn)), w0, w1);
+            unf2(fma2(p2, f2(vz, vz), f2(z[nt][0], z[nt][1])), z0, z1);
+            if (MASK) {                              // a masked key's scale may be anything
+              if (x0 == -INFINITY) { w0 = 0.f; z0 = z[nt][0]; }
+              if (x1 == -INFINITY) { w1 = 0.f; z1 = z[nt][1]; }
+            }
+            z[nt][0] = z0;
+            z[nt][1] = z1;
+            w[half] = pack_f16x2(w0, w1);
+          } else if constexpr (PBF16) {
+            split_bf16x2(make_float2(p0, p1), w[half], wl[half]);
           } else {
-            w[e] = pr;
+            w[half] = pack_f16x2(p0, p1);
           }
         }
-        if constexpr (BITS == 16 && PBF16) {
-          uint32_t h0, l0, h1, l1;
-          split_bf16x2(make_float2(w[0], w[1]), h0, l0);
-          split_bf16x2(make_float2(w[2], w[3]), h1, l1);
-          pb[nt][0] = movmatrix_t(h0);
-          pb[nt][1] = movmatrix_t(h1);
-          pl[nt][0] = movmatrix_t(l0);
-          pl[nt][1] = movmatrix_t(l1);
-        } else {
-          pb[nt][0] = movmatrix_t(pack_f16x2(w[0], w[1]));
-          pb[nt][1] = movmatrix_t(pack_f16x2(w[2], w[3]));
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          pb[f][nt][half] = movmatrix_t(w[half]);
+          if constexpr (BITS == 16 && PBF16) pl[f][nt][half] = movmatrix_t(wl[half]);
         }
       }
-      uint32_t a[MT][4];
-      load_v(vbase, kb, g, t, a);
+    }
+    auto add = [&](int blk, const uint32_t (&a)[MT][4]) {
+      const int f = blk / X, x = blk % X;
+      uint32_t px[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        px[nt][0] = X == 1 || g / GP == x ? pb[f][nt][0] : 0u;
+        px[nt][1] = X == 1 || g / GP == x ? pb[f][nt][1] : 0u;
+      }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           if constexpr (BITS == 16 && PBF16) {
-            mma_bf16_16816(o[mt][nt], a[mt], pb[nt]);
-            mma_bf16_16816(o[mt][nt], a[mt], pl[nt]);
+            mma_bf16_16816(o[mt][nt], a[mt], px[nt]);
+            mma_bf16_16816(o[mt][nt], a[mt], pl[f][nt]);
           } else {
-            mma_f16_16816(o[mt][nt], a[mt], pb[nt]);
+            mma_f16_16816(o[mt][nt], a[mt], px[nt]);
           }
         }
+    };
+    if constexpr (LDSM) {
+#pragma unroll
+      for (int blk = 0; blk < S::KB; blk += BPL) {
+        uint32_t w[BPL][2][D / 32];
+        load_v4(vbase, blk, lane, w);
+#pragma unroll
+        for (int i = 0; i < BPL; ++i) {
+          uint32_t a[MT][4];
+          spread_v(w[i], a);
+          add(blk + i, a);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int blk = 0; blk < S::KB; ++blk) {
+        uint32_t a[MT][4];
+        load_v(vbase, blk, g, t, a);
+        add(blk, a);
+      }
     }
   }
 
-  // l and z over the lanes of a row; o in the values' units, the zeros' share added
+  // New running maxima (scores c, less the old ones, are taken down with them) and, 4 bits, a new
+  // power of two of the value scales.
+  __device__ __forceinline__ void raise(float (&c)[SF][NT][4], float vtop) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int col = 0; col < 2; ++col) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int f = 0; f < SF; ++f) mx = fmaxf(mx, fmaxf(c[f][nt][col], c[f][nt][2 + col]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        const float old = m[nt][col];
+        // (a row without a visible key keeps m and its sums of zero)
+        const float now = mx == -INFINITY ? old : (first ? old + mx : fmaxf(old, old + mx));
+        const float al = first ? 0.f : ex2(old - now);
+        m[nt][col] = now;
+        l[nt][col] *= al;
+        z[nt][col] *= al;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          o[mt][nt][col] *= al;
+          o[mt][nt][2 + col] *= al;
+        }
+#pragma unroll
+        for (int f = 0; f < SF; ++f) {
+          c[f][nt][col] = (c[f][nt][col] + old) - now;
+          c[f][nt][2 + col] = (c[f][nt][2 + col] + old) - now;
+        }
+      }
+    first = false;
+    if constexpr (BITS == 4) {
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
+      if (vtop * nrm > 128.f) {
+        const int e = static_cast<int>((__float_as_uint(vtop) >> 23) & 255u) - 127;
+        const float nn = __uint_as_float(static_cast<uint32_t>(6 - e + 127) << 23);
+        const float f = nn / nrm;
+        nrm = nn;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e4 = 0; e4 < 4; ++e4) o[mt][nt][e4] *= f;
+      }
+    }
+  }
+
+  // l and z over the lanes of a row; o in the values' units, the zeros' share added; the column
+  // groups joined (every group's lanes then hold the rows' results)
   __device__ __forceinline__ void finish() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -564,6 +688,28 @@ struct Core {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[mt][nt][e] = fmaf(o[mt][nt][e], e < 2 ? f0 : f1, z[nt][e & 1]);
+    }
+    if constexpr (X > 1) {
+#pragma unroll
+      for (int off = GP / 2; off < 4; off <<= 1)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float om = __shfl_xor_sync(0xffffffffu, m[0][e], off);
+          const float ol = __shfl_xor_sync(0xffffffffu, l[0][e], off);
+          // a group without a key (l = 0) has no maximum
+          const float mm = l[0][e] == 0.f ? om : (ol == 0.f ? m[0][e] : fmaxf(m[0][e], om));
+          const float fa = l[0][e] == 0.f ? 0.f : ex2(m[0][e] - mm);
+          const float fb = ol == 0.f ? 0.f : ex2(om - mm);
+          m[0][e] = mm;
+          l[0][e] = l[0][e] * fa + ol * fb;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float other = __shfl_xor_sync(0xffffffffu, o[mt][0][2 * i + e], off);
+              o[mt][0][2 * i + e] = o[mt][0][2 * i + e] * fa + other * fb;
+            }
+        }
     }
   }
 };
@@ -593,56 +739,139 @@ __device__ __forceinline__ void store_row(const Rows &o, __nv_bfloat16 *o_lo, si
   }
 }
 
-template <int D, int BITS, int NT, bool QBF16, bool PBF16>
-__global__ void __launch_bounds__(32 * kWarps) paged_attention_kernel(const __grid_constant__ AttnParams p) {
-  using C = Core<D, BITS, NT, QBF16, PBF16>;
+// What a warp's run left of an item it did not cover.
+enum : int { kNone = 0, kOpen = 1, kEnds = 2 };      // kEnds: the piece has the item's last tile
+struct PieceAt {
+  int state, b, h, rt;
+  const float *at;               // [R][D] sums, [R][2] maximum and sum
+};
+
+// (m, l, acc) joined with another piece of the same row.  A piece without a visible key has l = 0
+// and no maximum.
+__device__ __forceinline__ void join(float &m, float &l, float4 &acc, float m2, float l2, const float4 &v) {
+  if (l2 == 0.f) return;
+  const float mn = l == 0.f ? m2 : fmaxf(m, m2);
+  const float fa = l == 0.f ? 0.f : ex2(m - mn), fb = ex2(m2 - mn);
+  m = mn;
+  l = l * fa + l2 * fb;
+  acc.x = acc.x * fa + v.x * fb;
+  acc.y = acc.y * fa + v.y * fb;
+  acc.z = acc.z * fa + v.z * fb;
+  acc.w = acc.w * fa + v.w * fb;
+}
+
+template <int D, int BITS, int R, bool QBF16, bool PBF16>
+__global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_attention_kernel(const __grid_constant__ AttnParams p) {
+  using C = Core<D, BITS, R, QBF16, PBF16>;
   using S = Shape<D, BITS>;
-  constexpr int R = 8 * NT, KT = S::KT, KTL = KT == 64 ? 6 : 5, ROWB = S::ROWB;
+  constexpr int NT = C::NT, KT = S::KT, KTL = S::KTL, ROWB = S::ROWB;
+  constexpr int PIECE = R * D + 2 * R;               // floats of a piece
+  static_assert(PIECE * 4 <= kStages * S::TILE, "a warp's ring holds a piece");
   extern __shared__ __align__(128) uint8_t smem[];
   int *pre = reinterpret_cast<int *>(smem + S::SMEM);          // [B + 1]
-  __shared__ int warp_sum[kWarps];
+  __shared__ int red[2][kWarps];
+  __shared__ PieceAt at_piece[kWarps][2];            // what each warp leaves in shared memory
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   pdl_launch_dependents();
   pdl_wait();
-  // units before each sequence: thread i sums a run of sequences, then a scan over the threads
+  if (lane < 2) at_piece[warp][lane].state = kNone;
   const int B = p.batch.B;
+  int pad, upw;
   {
+    // the line's length and the number of items, then the padding, then the units before each
+    // sequence; thread i takes a run of sequences (a single one up to 128: kept in registers)
     const int per = (B + 32 * kWarps - 1) / (32 * kWarps);
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
-    int sum = 0;
+    PagedSeq mine = {0, 0, 0};
+    int tiles = 0, items = 0;
     for (int b = b0; b < b1; ++b) {
-      const int u = p.Hkv * units_per_head(paged_seq(p.batch, b, p.status), R, p.G, KTL);
-      pre[b + 1] = u;
-      sum += u;
+      mine = paged_seq(p.batch, b, p.status);
+      const int rts = row_tiles(mine, R, p.G);
+      items += rts;
+      for (int rt = 0; rt < rts; ++rt) tiles += tiles_of(mine, rt, R, p.by_g, KTL);
     }
-    int inc = sum;
+    const int wt = __reduce_add_sync(0xffffffffu, tiles), wi = __reduce_add_sync(0xffffffffu, items);
+    if (lane == 0) {
+      red[0][warp] = wt;
+      red[1][warp] = wi;
+    }
+    __syncthreads();
+    tiles = items = 0;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += x;
+    for (int w = 0; w < kWarps; ++w) {
+      tiles += red[0][w];
+      items += red[1][w];
     }
-    if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    int run = inc - sum;
-    for (int w = 0; w < warp; ++w) run += warp_sum[w];
-    if (tid == 0) pre[0] = 0;
-    for (int b = b0; b < b1; ++b) {
-      run += pre[b + 1];
-      pre[b + 1] = run;
+    tiles *= p.Hkv;
+    items *= p.Hkv;
+    // few items: runs of q tiles, every item rounded up to whole runs.  Rounding adds half a run
+    // per item on average, so q is tried for 5/8 of one and, where that does not fit the warps,
+    // taken for a whole one, which always does.
+    const bool few = !p.whole && 2 * items <= p.warps;
+    if (p.whole) {
+      pad = p.whole;
+      upw = pad * ((items + p.warps - 1) / p.warps);
+    } else {
+      const int w = p.warps - (few ? items * 5 / 8 : 0);
+      upw = max(1, (tiles + w - 1) / w);
+      pad = few ? upw : 1;
+    }
+    for (int attempt = 0;; ++attempt) {
+      const float rpad = 1.f / pad;
+      int sum = 0;
+      for (int b = b0; b < b1; ++b) {
+        if (per > 1) mine = paged_seq(p.batch, b, nullptr);
+        const int rts = row_tiles(mine, R, p.G);
+        int u = 0;
+        for (int rt = 0; rt < rts; ++rt) u += padded(tiles_of(mine, rt, R, p.by_g, KTL), pad, rpad);
+        u *= p.Hkv;
+        pre[b + 1] = u;
+        sum += u;
+      }
+      int inc = sum;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += x;
+      }
+      __syncthreads();                               // red is read
+      if (lane == 31) red[0][warp] = inc;
+      __syncthreads();
+      int run = inc - sum, all = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) run += red[0][w];
+        all += red[0][w];
+      }
+      if (attempt == 0 && few && all > static_cast<long long>(upw) * p.warps) {
+        const int w = p.warps - items;
+        pad = upw = max(1, (tiles + w - 1) / w);
+        continue;
+      }
+      if (tid == 0) pre[0] = 0;
+      for (int b = b0; b < b1; ++b) {
+        run += pre[b + 1];
+        pre[b + 1] = run;
+      }
+      break;
     }
     __syncthreads();
-    if (blockIdx.x == 0)
-      for (int b = tid; b <= B; b += 32 * kWarps) p.pre[b] = pre[b];
+    if (blockIdx.x == 0) {
+      for (int b = tid; b <= B; b += 32 * kWarps) p.plan[b] = pre[b];
+      if (tid == 0) {
+        p.plan[B + 1] = upw;
+        p.plan[B + 2] = pad;
+      }
+    }
   }
+  const float rpad = 1.f / pad;
   const int total = pre[B];
   const int w = blockIdx.x * kWarps + warp;
-  const int upw = (total + p.warps - 1) / p.warps;
-  int u = min(static_cast<long long>(total), static_cast<long long>(w) * upw);
-  const int uend = min(total, u + upw);
+  int u = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(w) * upw));
+  const int uend = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(w + 1) * upw));
   const uint32_t ring = smem_u32(smem) + warp * kStages * S::TILE;
   uint8_t *ring_p = smem + warp * kStages * S::TILE;
-  const uint64_t pol = l2_evict_first_policy();
-  (void)pol;
+  C core;
 
   while (u < uend) {
     int b;
@@ -655,19 +884,26 @@ __global__ void __launch_bounds__(32 * kWarps) paged_attention_kernel(const __gr
       }
       b = lo;
     }
-    const PagedSeq s = paged_seq(p.batch, b, p.status);
-    const int per_head = (pre[b + 1] - pre[b]) / p.Hkv;
-    const int h = (u - pre[b]) / per_head;
-    int t0 = (u - pre[b]) % per_head, rt = 0, T;
-    while (t0 >= (T = tiles_of(s, rt, R, p.G, KTL))) {
-      t0 -= T;
+    const PagedSeq s = paged_seq(p.batch, b, nullptr);
+    const int per_head = div(pre[b + 1] - pre[b], p.by_hkv);
+    const int h = div(u - pre[b], per_head, 1.f / per_head);
+    int t0 = u - pre[b] - h * per_head, rt = 0, T, TP;
+    while (true) {
+      T = tiles_of(s, rt, R, p.by_g, KTL);
+      TP = padded(T, pad, rpad);
+      if (t0 < TP) break;
+      t0 -= TP;
       ++rt;
     }
-    const int t1 = min(T, t0 + (uend - u));
-    u += t1 - t0;
+    const int step = min(TP - t0, uend - u);
+    const int t1 = min(T, t0 + step);
+    u += step;
     const int rows = s.n * p.G, r0 = rt * R;
 
-    // ---- copies of tile `i` into its slot; the next tile's pages are looked up one tile ahead
+    // ---- everything the first products wait for is asked for at once: the queries, the pages
+    // of the first tiles (and of the next one later, a tile ahead of its copies)
+    typename C::Raw qraw;
+    C::load_q(p, s, b, h, r0, rows, g, t, qraw);
     auto look = [&](int i) {                         // lane kb < KB: first row of block kb, or -1
       const int key = i * KT + lane * 16;
       int row = -1;
@@ -678,58 +914,79 @@ __global__ void __launch_bounds__(32 * kWarps) paged_attention_kernel(const __gr
       }
       return row;
     };
-    int next = look(t0);
-    auto issue = [&](int i, int slot) {
-      if (i < t1) {
-        const int rows16 = next;
-        next = look(i + 1);
-        uint8_t *kd = ring_p + slot * S::TILE, *vd = kd + KT * ROWB, *sd = vd + KT * ROWB;
+    int ahead[kStages];
 #pragma unroll
-        for (int j = 0; j < KT * ROWB / 512; ++j) {
-          const int cidx = j * 32 + lane, blk = cidx / ROWB, cb = cidx % ROWB;
-          const int row = __shfl_sync(0xffffffffu, rows16, blk);
-          bool ok = row >= 0;
-          int dst = cidx;
-          if constexpr (BITS == 16) {
-            constexpr int CPR = D / 8;
-            const int key = cidx / CPR;
-            ok = ok && i * KT + key < s.len;         // nothing of a row without a token is used
-            dst = piece16<D>(key, cidx % CPR);
+    for (int i = 0; i < kStages; ++i) ahead[i] = look(t0 + i);
+    int next = ahead[kStages - 1];
+    auto copy = [&](int i, int slot, int rows16) {
+      if (i < t1) {
+        uint8_t *kd = ring_p + slot * S::TILE, *vd = kd + KT * ROWB, *sd = vd + KT * ROWB;
+        const int sdst = BITS == 4 ? lane ^ (((lane >> 3) & 1) << 2) : 0;   // scale_at, in 16 bytes
+        if (p.page_log2 >= KTL) {                    // the tile is one run of rows of a page
+          const int row = __shfl_sync(0xffffffffu, rows16, 0);
+          const uint8_t *ks = p.k + static_cast<size_t>(max(row, 0)) * ROWB + lane * 16;
+          const uint8_t *vs = p.v + static_cast<size_t>(max(row, 0)) * ROWB + lane * 16;
+#pragma unroll
+          for (int j = 0; j < KT * ROWB / 512; ++j) {
+            const int cidx = j * 32 + lane;
+            bool ok = row >= 0;
+            int dst = BITS == 4 && D >= 32 ? piece4<D>(cidx / (D / 32), cidx % (D / 32)) : cidx;
+            if constexpr (BITS == 16) {
+              ok = ok && i * KT + cidx / (D / 8) < s.len;   // nothing of a row without a token is used
+              dst = piece16<D>(cidx / (D / 8), cidx % (D / 8));
+            }
+            cp_async16_zfill(kd + dst * 16, ks + j * 512, ok);
+            cp_async16_zfill(vd + dst * 16, vs + j * 512, ok);
           }
-          const size_t src = static_cast<size_t>(max(row, 0)) * ROWB + cb * 16;
-          cp_async16_zfill(kd + dst * 16, p.k + src, ok);
-          cp_async16_zfill(vd + dst * 16, p.v + src, ok);
-        }
-        if constexpr (BITS == 4) {
-          const int row = __shfl_sync(0xffffffffu, rows16, lane >> 3);
-          cp_async16_zfill(sd + lane * 16, p.scales + static_cast<size_t>(max(row, 0)) + (lane & 7) * 2,
-                           row >= 0);
+          if constexpr (BITS == 4)
+            cp_async16_zfill(sd + sdst * 16, p.scales + static_cast<size_t>(max(row, 0)) + lane * 2, row >= 0);
+        } else {                                     // 16-row blocks, each within a page
+#pragma unroll
+          for (int j = 0; j < KT * ROWB / 512; ++j) {
+            const int cidx = j * 32 + lane, blk = cidx / ROWB, cb = cidx % ROWB;
+            const int row = __shfl_sync(0xffffffffu, rows16, blk);
+            bool ok = row >= 0;
+            int dst = BITS == 4 && D >= 32 ? piece4<D>(cidx / (D / 32), cidx % (D / 32)) : cidx;
+            if constexpr (BITS == 16) {
+              ok = ok && i * KT + cidx / (D / 8) < s.len;
+              dst = piece16<D>(cidx / (D / 8), cidx % (D / 8));
+            }
+            const size_t src = static_cast<size_t>(max(row, 0)) * ROWB + cb * 16;
+            cp_async16_zfill(kd + dst * 16, p.k + src, ok);
+            cp_async16_zfill(vd + dst * 16, p.v + src, ok);
+          }
+          if constexpr (BITS == 4) {
+            const int row = __shfl_sync(0xffffffffu, rows16, lane >> 3);
+            cp_async16_zfill(sd + sdst * 16, p.scales + static_cast<size_t>(max(row, 0)) + (lane & 7) * 2,
+                             row >= 0);
+          }
         }
       }
       cp_async_commit();
     };
     __syncwarp();                                    // the ring's last readers are done
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(t0 + i, i);
+    for (int i = 0; i < kStages - 1; ++i) copy(t0 + i, i, ahead[i]);
 
-    C core;
     core.reset();
-    core.load_q(p, s, b, h, r0, rows, g, t);
+    core.set_q(p, qraw, g, t);
     int lim[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int tok = min(s.n - 1, (r0 + nt * 8 + 2 * t + e) / p.G);
+        const int tok = min(s.n - 1, div(r0 + C::row_of(nt, 2 * t + e), p.by_g));
         lim[nt][e] = min(s.len, s.len - s.n + tok + 1);
       }
-    const int first_lim = min(s.len, s.len - s.n + r0 / p.G + 1);   // of the tile's first row
+    const int first_lim = min(s.len, s.len - s.n + div(r0, p.by_g) + 1);   // of the tile's first row
 
     int slot = 0;
     for (int i = t0; i < t1; ++i) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();
-      issue(i + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
+      const int rows16 = next;
+      next = look(i + kStages);
+      copy(i + kStages - 1, slot == 0 ? kStages - 1 : slot - 1, rows16);
       const uint32_t kb = ring + slot * S::TILE, vb = kb + KT * ROWB, sb = vb + KT * ROWB;
       if ((i + 1) * KT <= first_lim) core.template tile<false>(kb, vb, sb, i * KT, lim, s.len, lane);
       else core.template tile<true>(kb, vb, sb, i * KT, lim, s.len, lane);
@@ -738,121 +995,205 @@ __global__ void __launch_bounds__(32 * kWarps) paged_attention_kernel(const __gr
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     core.finish();
 
-    const bool whole = t0 == 0 && t1 == T;
-    constexpr int N = D / 8;
+    PieceAt me;
+    me.state = t1 == T ? kEnds : kOpen;
+    me.b = b;
+    me.h = h;
+    me.rt = rt;
+    if (t0 == 0 && t1 == T) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int rr = nt * 8 + 2 * t + e, r = r0 + rr;
-        if (r >= rows) continue;
-        float v[N];
-#pragma unroll
-        for (int mt = 0; mt < C::MT; ++mt) {
-          v[2 * mt] = core.o[mt][nt][e];
-          v[2 * mt + 1] = core.o[mt][nt][2 + e];
-        }
-        if (whole) {
+        for (int e = 0; e < 2; ++e) {
+          const int r = r0 + C::row_of(nt, 2 * t + e);
+          if (r >= rows || 2 * t + e >= C::GP) continue;
           const float inv = core.l[nt][e] == 0.f ? 0.f : 1.f / core.l[nt][e];
+          const size_t off = out_offset(p, s, b, h, r);
 #pragma unroll
-          for (int x = 0; x < N; ++x) v[x] = core.l[nt][e] == 0.f ? 0.f : v[x] * inv;
-          store_row<N>(p.o, p.o_lo,
-                       row_offset(p.o, p.batch.cu != nullptr, s, b, r / p.G, h * p.G + r % p.G) + g * N, v);
-        } else {
-          const size_t at = (static_cast<size_t>(w) * 2 + (t0 == 0 ? 1 : 0)) * R + rr;
-          float *d = p.part_o + at * D + g * N;
+          for (int c = 0; c < C::CH; ++c) {
+            float v[C::N];
 #pragma unroll
-          for (int x = 0; x < N; x += 2) *reinterpret_cast<float2 *>(d + x) = make_float2(v[x], v[x + 1]);
-          if (g == 0) p.part_ml[at] = make_float2(core.m[nt][e], core.l[nt][e]);
+            for (int x = 0; x < C::N; ++x)
+              v[x] = core.l[nt][e] == 0.f ? 0.f : core.o[c * 2 + (x >> 1)][nt][2 * (x & 1) + e] * inv;
+            store_row<C::N>(p.o, p.o_lo, off + C::ch0(c, g), v);
+          }
         }
+    } else {
+      // a piece waits where the ring was if it is the run's last (a begun item always is); a
+      // first one with more of the run to come goes to the warp's place in the workspace
+      const int k = t0 == 0 ? 1 : 0;
+      float *d = u >= uend ? reinterpret_cast<float *>(ring_p) : p.spill + static_cast<size_t>(w) * PIECE;
+      me.at = d;
+      if (lane == 0) at_piece[warp][k] = me;
+      __syncwarp();                                  // the ring is read
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int rr = C::row_of(nt, 2 * t + e);
+          if (2 * t + e >= C::GP) continue;
+#pragma unroll
+          for (int c = 0; c < C::CH; ++c)
+#pragma unroll
+            for (int x = 0; x < C::N; ++x)
+              d[rr * D + C::ch0(c, g) + x] = core.o[c * 2 + (x >> 1)][nt][2 * (x & 1) + e];
+          if (g == 0) {
+            d[R * D + 2 * rr] = core.m[nt][e];
+            d[R * D + 2 * rr + 1] = core.l[nt][e];
+          }
+        }
+    }
+  }
+  __syncthreads();
+
+  // ---- join the pieces that follow one another in this CTA: a chain starts with warp 0's piece
+  // of an item begun elsewhere or with any warp's piece that begins an item, and goes on with the
+  // next warps' until one ends the item
+  for (int c = 0; c <= kWarps; ++c) {
+    const int wa = c == 0 ? 0 : c - 1, ka = c == 0 ? 0 : 1;
+    if (at_piece[wa][ka].state == kNone) continue;
+    int wz = wa, ends = at_piece[wa][ka].state == kEnds;
+    while (!ends && wz + 1 < kWarps && at_piece[wz + 1][0].state != kNone) {
+      ++wz;
+      ends = at_piece[wz][0].state == kEnds;
+    }
+    const PieceAt it = at_piece[wa][ka];
+    const PagedSeq s = paged_seq(p.batch, it.b, nullptr);
+    const int rows = s.n * p.G;
+    for (int e = tid; e < R * (D / 4); e += 32 * kWarps) {
+      const int rr = e / (D / 4), c4 = e % (D / 4) * 4, r = it.rt * R + rr;
+      if (r >= rows) continue;
+      float m = 0.f, l = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int x = wa; x <= wz; ++x) {
+        const float *d = at_piece[x][x == wa ? ka : 0].at;
+        join(m, l, acc, d[R * D + 2 * rr], d[R * D + 2 * rr + 1],
+             *reinterpret_cast<const float4 *>(d + rr * D + c4));
       }
+      if (ka == 1 && ends) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float v[4] = {l == 0.f ? 0.f : acc.x * inv, l == 0.f ? 0.f : acc.y * inv,
+                            l == 0.f ? 0.f : acc.z * inv, l == 0.f ? 0.f : acc.w * inv};
+        store_row<4>(p.o, p.o_lo,
+                     out_offset(p, s, it.b, it.h, r) + c4, v);
+      } else {
+        const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + ka) * R + rr;
+        *reinterpret_cast<float4 *>(p.part_o + at * D + c4) = acc;
+        if (c4 == 0) p.part_ml[at] = make_float2(m, l);
+      }
+    }
   }
 }
 
-// Joins the pieces of the items that more than one warp worked on.  One CTA per (row of a tile,
-// head, sequence): D / 4 lanes hold the row's channels, the CTA's lane groups take pieces in turn
-// and are added in a fixed order.
-template <int D, int NT, int KTL>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int R = 8 * NT, LN = D / 4, GR = 128 / LN;
-  __shared__ float so[GR][D];
-  __shared__ float2 sml[GR];
-  const int rr = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const int grp = threadIdx.x / LN, ln = threadIdx.x % LN;
+// Joins the pieces of the items that more than one CTA worked on: WPR warps per (row of a tile,
+// head, sequence).  D / 4 lanes hold the row's channels; the lane groups take pieces in turn and
+// are added in a fixed order.
+template <int D, int R, int KTL, int WPR>
+__global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ AttnParams p, int rows_max) {
+  constexpr int LN = D / 4, GW = 32 / LN, GR = GW * WPR, UN = 4;   // UN pieces in flight per group
+  __shared__ float so[WPR == 4 ? 4 : 1][D];
+  __shared__ float2 sml[4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int unit = WPR == 4 ? blockIdx.x : blockIdx.x * 4 + warp;
+  const int h = unit / rows_max, rr = unit - h * rows_max, b = blockIdx.y;
+  const int ln = lane % LN, grp = (WPR == 4 ? warp * GW : 0) + lane / LN;
   pdl_launch_dependents();
   pdl_wait();
+  if (h >= p.Hkv) return;
   const PagedSeq s = paged_seq(p.batch, b, nullptr);
+  const int p0 = p.plan[b], p1 = p.plan[b + 1], upw = p.plan[p.batch.B + 1], pad = p.plan[p.batch.B + 2];
   const int rows = s.n * p.G, rts = row_tiles(s, R, p.G);
   if (rr >= rows) return;
-  const int total = p.pre[p.batch.B], upw = (total + p.warps - 1) / p.warps;
-  int u0 = p.pre[b] + h * ((p.pre[b + 1] - p.pre[b]) / p.Hkv);
+  const float rpad = 1.f / pad;
+  int u0 = p0 + h * div(p1 - p0, p.by_hkv);
   for (int rt = 0; rt < rts; ++rt) {
-    const int T = tiles_of(s, rt, R, p.G, KTL);
-    const int w0 = u0 / upw, w1 = (u0 + T - 1) / upw, r = rt * R + rr;
-    u0 += T;
-    if (w0 == w1 || r >= rows) continue;
-    float m = -INFINITY, l = 0.f;
+    const int T = tiles_of(s, rt, R, p.by_g, KTL);
+    const int ca = u0 / upw / kWarps, cz = (u0 + T - 1) / upw / kWarps, r = rt * R + rr;
+    u0 += padded(T, pad, rpad);
+    if (ca == cz || r >= rows) continue;
+    float m = 0.f, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w = w0 + grp; w <= w1; w += GR) {
-      const size_t at = (static_cast<size_t>(w) * 2 + (w == w0 ? 1 : 0)) * R + rr;
-      const float2 ml = p.part_ml[at];
-      const float4 v = *reinterpret_cast<const float4 *>(p.part_o + at * D + ln * 4);
-      if (ml.y == 0.f && ml.x == -INFINITY) continue;      // no visible key in this piece
-      const float mn = fmaxf(m, ml.x);
-      const float fa = m == -INFINITY ? 0.f : ex2(m - mn), fb = ex2(ml.x - mn);
-      m = mn;
-      l = l * fa + ml.y * fb;
-      acc.x = acc.x * fa + v.x * fb;
-      acc.y = acc.y * fa + v.y * fb;
-      acc.z = acc.z * fa + v.z * fb;
-      acc.w = acc.w * fa + v.w * fb;
-    }
-    __syncthreads();
-    *reinterpret_cast<float4 *>(&so[grp][ln * 4]) = acc;
-    if (ln == 0) sml[grp] = make_float2(m, l);
-    __syncthreads();
-    if (threadIdx.x < LN) {
-      float M = -INFINITY, L = 0.f;
-      for (int i = 0; i < GR; ++i) M = fmaxf(M, sml[i].x);
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int i = 0; i < GR; ++i) {
-        if (sml[i].x == -INFINITY && sml[i].y == 0.f) continue;
-        const float f = ex2(sml[i].x - M);
-        L = fmaf(sml[i].y, f, L);
+    for (int c0 = ca + grp; c0 <= cz; c0 += UN * GR) {
+      float2 ml[UN];
+      float4 v[UN];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = fmaf(so[i][ln * 4 + j], f, v[j]);
+      for (int i = 0; i < UN; ++i) {
+        const int c = c0 + i * GR;
+        const size_t at = (static_cast<size_t>(min(c, cz)) * 2 + (c == ca ? 1 : 0)) * R + rr;
+        ml[i] = c <= cz ? p.part_ml[at] : make_float2(0.f, 0.f);
+        v[i] = c <= cz ? *reinterpret_cast<const float4 *>(p.part_o + at * D + ln * 4)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = L == 0.f ? 0.f : v[j] / L;
-      store_row<4>(p.o, p.o_lo,
-                   row_offset(p.o, p.batch.cu != nullptr, s, b, r / p.G, h * p.G + r % p.G) + ln * 4, v);
+      for (int i = 0; i < UN; ++i) join(m, l, acc, ml[i].x, ml[i].y, v[i]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int off = LN; off < 32; off <<= 1) {        // the warp's groups, lower first
+      const float m2 = __shfl_down_sync(0xffffffffu, m, off), l2 = __shfl_down_sync(0xffffffffu, l, off);
+      float4 v;
+      v.x = __shfl_down_sync(0xffffffffu, acc.x, off);
+      v.y = __shfl_down_sync(0xffffffffu, acc.y, off);
+      v.z = __shfl_down_sync(0xffffffffu, acc.z, off);
+      v.w = __shfl_down_sync(0xffffffffu, acc.w, off);
+      join(m, l, acc, m2, l2, v);
+    }
+    if constexpr (WPR == 4) {
+      __syncthreads();
+      if (lane < LN) *reinterpret_cast<float4 *>(&so[warp][ln * 4]) = acc;
+      if (lane == 0) sml[warp] = make_float2(m, l);
+      __syncthreads();
+      if (warp == 0 && lane < LN)
+#pragma unroll
+        for (int i = 1; i < 4; ++i)
+          join(m, l, acc, sml[i].x, sml[i].y, *reinterpret_cast<const float4 *>(&so[i][ln * 4]));
+    }
+    if ((WPR == 1 || warp == 0) && lane < LN) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float v[4] = {l == 0.f ? 0.f : acc.x * inv, l == 0.f ? 0.f : acc.y * inv,
+                          l == 0.f ? 0.f : acc.z * inv, l == 0.f ? 0.f : acc.w * inv};
+      store_row<4>(p.o, p.o_lo, out_offset(p, s, b, h, r) + ln * 4, v);
     }
   }
 }
 
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// Row tiles of 8, 16 or 32 rows by the rows of an average sequence: a tile's keys are read and
-// unpacked once for all its rows.  16 at d~ = 128, where 32 rows' accumulators would not fit the
-// registers.
-int pick_nt(const PagedArgs &a) {
+// Rows of a tile, by the rows of an average sequence: a tile's keys are read and unpacked once
+// for all its rows, and a 4-bit tile of fewer than 8 rows scores several key blocks at a time.
+// 16 at most at d~ = 128, where 32 rows' accumulators would not fit the registers.
+int pick_rows(const PagedArgs &a) {
   const long long per = (static_cast<long long>(a.tokens) + a.B - 1) / a.B * (a.H / a.Hkv);
-  if (per <= 8) return 1;
-  if (per <= 16 || a.D == 128) return 2;
-  return 4;
+  if (a.bits == 4 && per <= 2) return 2;
+  if (a.bits == 4 && per <= 4) return 4;
+  if (per <= 8) return 8;
+  if (per <= 16 || a.D == 128) return 16;
+  return 32;
 }
 
-int key_tile_log2(const PagedArgs &a) { return a.bits == 16 && a.D == 128 ? 5 : 6; }
+int key_tile_log2(const PagedArgs &a) {
+  return a.bits == 16 && a.D >= 64 ? (a.D == 128 ? 4 : 5) : 6;     // Shape::KTL
+}
 
-// Warps of a launch: as many CTAs as fit the device at once by shared memory (227 KB an SM; the
-// registers allow as many), but no more than the units there can be.
-int plan_ctas(const PagedArgs &a) {
+// CTAs of a launch: as many as the device holds at once by registers and shared memory (227 KB
+// an SM), but no more than the units there can be.
+// Shared memory of a CTA: the rings and the units before each sequence.
+size_t attn_smem(const PagedArgs &a) {
   const int rowb = a.bits == 4 ? a.D / 2 : 2 * a.D, kt = 1 << key_tile_log2(a);
-  const size_t smem = static_cast<size_t>(kWarps) * kStages * kt * (2 * rowb + (a.bits == 4 ? 8 : 0)) +
-                      (a.B + 1) * 4 + 1024;
-  const int nt = pick_nt(a);
-  const int by_regs = nt == 1 ? 4 : (nt == 2 ? 3 : 2);
-  long long per_sm = (227 * 1024) / static_cast<long long>(smem);
+  return static_cast<size_t>(kWarps) * kStages * kt * (2 * rowb + (a.bits == 4 ? 8 : 0)) +
+         (static_cast<size_t>(a.B) + 1) * 4;
+}
+
+// Items of up to 256 tokens are not split (0: they may be): a warp walks four tiles in less than
+// the merge kernel takes to start, so it is not launched then.
+int whole_tiles(const PagedArgs &a) {
+  const long long cap = static_cast<long long>(a.max_pages) << a.page_log2;
+  return cap <= 256 ? static_cast<int>((cap + (1 << key_tile_log2(a)) - 1) >> key_tile_log2(a)) : 0;
+}
+
+int plan_ctas(const PagedArgs &a) {
+  long long per_sm = (227 * 1024) / static_cast<long long>(attn_smem(a) + 2048);
+  const int by_regs = ctas_by_regs(a.D, a.bits, pick_rows(a));
   if (per_sm > by_regs) per_sm = by_regs;
   if (per_sm < 1) per_sm = 1;
   const long long units = paged_attention_units(a);
@@ -862,49 +1203,58 @@ int plan_ctas(const PagedArgs &a) {
 }
 
 struct AttnLayout {
-  size_t pre, ml, o, total;
+  size_t plan, ml, o, spill, total;
 };
 AttnLayout attn_layout(const PagedArgs &a, int ctas) {
   AttnLayout L;
-  const size_t rows = static_cast<size_t>(ctas) * kWarps * 2 * 8 * pick_nt(a);
-  L.pre = 0;
-  L.ml = align256(static_cast<size_t>(a.B + 1) * 4);
+  const size_t rows = static_cast<size_t>(ctas) * 2 * pick_rows(a);
+  L.plan = 0;
+  L.ml = align256(static_cast<size_t>(a.B + 3) * 4);
   L.o = L.ml + align256(rows * 8);
-  L.total = L.o + align256(rows * a.D * 4);
+  L.spill = L.o + align256(rows * a.D * 4);
+  L.total = L.spill + align256(static_cast<size_t>(ctas) * kWarps * pick_rows(a) * (a.D + 2) * 4);
   return L;
 }
 
-template <int D, int BITS, int NT, bool QBF16, bool PBF16>
+template <int D, int BITS, int R, bool QBF16, bool PBF16>
 cudaError_t launch(const PagedArgs &a, const AttnParams &p, int ctas, cudaStream_t st) {
-  const size_t smem = Shape<D, BITS>::SMEM + static_cast<size_t>(a.B + 1) * 4;
-  cudaError_t e = ensure_dyn_smem<paged_attention_kernel<D, BITS, NT, QBF16, PBF16>>(smem);
+  const size_t smem = attn_smem(a);
+  cudaError_t e = ensure_dyn_smem<paged_attention_kernel<D, BITS, R, QBF16, PBF16>>(smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_attention_kernel<D, BITS, NT, QBF16, PBF16>, dim3(ctas), dim3(32 * kWarps),
+  e = launch_pdl(paged_attention_kernel<D, BITS, R, QBF16, PBF16>, dim3(ctas), dim3(32 * kWarps),
                  smem, st, p);
-  if (e != cudaSuccess) return e;
-  const long long rows = static_cast<long long>(a.tokens) * p.G;
-  const unsigned gx = static_cast<unsigned>(rows < 8 * NT ? rows : 8 * NT);
-  return launch_pdl(paged_merge_kernel<D, NT, Shape<D, BITS>::KT == 64 ? 6 : 5>,
-                    dim3(gx, a.Hkv, a.B), dim3(128), 0, st, p);
+  if (e != cudaSuccess || p.whole) return e;
+  // rows a tile can have: all of them, or a uniform batch's
+  const long long rows = static_cast<long long>(a.cu ? a.tokens : a.tokens / a.B) * p.G;
+  const int rm = static_cast<int>(rows < R ? rows : R);
+  // few rows have many pieces each: a CTA a row, else a warp
+  constexpr int KTL = Shape<D, BITS>::KTL;
+  const long long units = static_cast<long long>(rm) * a.Hkv;
+  if (units * a.B <= 4LL * num_sms())
+    return launch_pdl(paged_merge_kernel<D, R, KTL, 4>, dim3(static_cast<unsigned>(units), a.B), dim3(128), 0, st, p, rm);
+  return launch_pdl(paged_merge_kernel<D, R, KTL, 1>, dim3(static_cast<unsigned>((units + 3) / 4), a.B), dim3(128), 0, st, p, rm);
 }
 
-template <int D, int NT>
+template <int D, int R>
 cudaError_t launch_typed(const PagedArgs &a, const AttnParams &p, int ctas, cudaStream_t st) {
-  if (a.bits == 16) {
-    if (a.page_f16) return launch<D, 16, NT, false, false>(a, p, ctas, st);
-    return launch<D, 16, NT, true, true>(a, p, ctas, st);
-  }
-  if (a.q.dtype == CCA_F16) return launch<D, 4, NT, false, false>(a, p, ctas, st);
-  return launch<D, 4, NT, true, false>(a, p, ctas, st);
+  if constexpr (R >= 8)
+    if (a.bits == 16)
+      return a.page_f16 ? launch<D, 16, R, false, false>(a, p, ctas, st)
+                        : launch<D, 16, R, true, true>(a, p, ctas, st);
+  if (a.bits != 4) return cudaErrorInvalidValue;
+  if (a.q.dtype == CCA_F16) return launch<D, 4, R, false, false>(a, p, ctas, st);
+  return launch<D, 4, R, true, false>(a, p, ctas, st);
 }
 
 template <int D>
 cudaError_t launch_rows(const PagedArgs &a, const AttnParams &p, int ctas, cudaStream_t st) {
-  switch (pick_nt(a)) {
-    case 1: return launch_typed<D, 1>(a, p, ctas, st);
+  switch (pick_rows(a)) {
     case 2: return launch_typed<D, 2>(a, p, ctas, st);
+    case 4: return launch_typed<D, 4>(a, p, ctas, st);
+    case 8: return launch_typed<D, 8>(a, p, ctas, st);
+    case 16: return launch_typed<D, 16>(a, p, ctas, st);
     default:
-      if constexpr (D < 128) return launch_typed<D, 4>(a, p, ctas, st);
+      if constexpr (D < 128) return launch_typed<D, 32>(a, p, ctas, st);
       return cudaErrorInvalidValue;
   }
 }
@@ -912,7 +1262,7 @@ cudaError_t launch_rows(const PagedArgs &a, const AttnParams &p, int ctas, cudaS
 }  // namespace
 
 long long paged_attention_units(const PagedArgs &a) {
-  const long long R = 8 * pick_nt(a), G = a.H / a.Hkv;
+  const long long R = pick_rows(a), G = a.H / a.Hkv;
   const long long cap = static_cast<long long>(a.max_pages) << a.page_log2;
   const long long tiles = (cap >> key_tile_log2(a)) + 1;
   const long long row_tiles = a.tokens * G / R + a.B;
@@ -941,14 +1291,18 @@ cudaError_t paged_attention(const PagedArgs &a, cudaStream_t st) {
   p.scales = static_cast<const uint2 *>(a.scales);
   p.table = a.table;
   p.status = a.status;
-  p.pre = reinterpret_cast<int *>(ws + L.pre);
+  p.plan = reinterpret_cast<int *>(ws + L.plan);
+  p.whole = whole_tiles(a);
   p.part_ml = reinterpret_cast<float2 *>(ws + L.ml);
   p.part_o = reinterpret_cast<float *>(ws + L.o);
+  p.spill = reinterpret_cast<float *>(ws + L.spill);
   p.max_pages = a.max_pages;
   p.n_pages = a.n_pages;
   p.page_log2 = a.page_log2;
   p.Hkv = a.Hkv;
   p.G = a.H / a.Hkv;
+  p.by_g = fast_div(p.G);
+  p.by_hkv = fast_div(a.Hkv);
   p.warps = ctas * kWarps;
   p.scale_log2 = static_cast<float>(a.scale * 1.4426950408889634);
   switch (a.D) {

@@ -1,0 +1,293 @@
+// Argument marshalling of the paged-cache calls from Python in native code: torch tensors become
+// cca_paged_cache_t / cca_rows_t, outputs and scratch are allocated on the current stream, and
+// the C entry point is called.  A serving step makes these calls once per layer and token, where
+// the same marshalling in Python takes longer than the kernels (about 20 us a call against 2).
+//
+// The entry points' addresses come from the library that the package loaded (bind()).  A call
+// returns its result, or the entry point's status as an int when that is not CCA_OK.
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "cca.h"
+
+namespace {
+
+decltype(&cca_paged_append) g_append = nullptr;
+decltype(&cca_paged_gather) g_gather = nullptr;
+decltype(&cca_paged_attention) g_attention = nullptr;
+decltype(&cca_paged_attention_workspace_size) g_attention_ws = nullptr;
+
+// What describe() packs into a bytes object: the C struct and the tensors' device.
+struct Desc {
+  cca_paged_cache_t c;
+  int device;
+};
+
+struct Invalid {
+  std::string what;
+};
+
+#define NEED(cond, msg) \
+  if (!(cond)) throw Invalid{msg}
+
+const at::Tensor *tensor(PyObject *o, const char *name) {
+  if (o == Py_None) return nullptr;
+  if (!THPVariable_Check(o)) throw Invalid{std::string(name) + " is not a tensor"};
+  return &THPVariable_Unpack(o);
+}
+
+const Desc &desc_of(PyObject *o) {
+  NEED(PyBytes_Check(o) && PyBytes_GET_SIZE(o) == sizeof(Desc), "not a cache description");
+  return *reinterpret_cast<const Desc *>(PyBytes_AS_STRING(o));
+}
+
+int dtype_of(at::ScalarType t) {
+  switch (t) {
+    case at::kFloat: return CCA_F32;
+    case at::kBFloat16: return CCA_BF16;
+    case at::kHalf: return CCA_F16;
+    default: return -1;
+  }
+}
+
+struct Tokens {
+  int64_t n;
+  int dims;
+  int64_t d0, d1;
+};
+
+Tokens tokens_of(const Desc &d, const at::Tensor &t, const void *cu) {
+  if (t.dim() == 3) return {t.size(0), 3, t.size(0), 0};
+  NEED(t.dim() == 4, "rows are [tokens, heads, d] or [batch, tokens, heads, d]");
+  NEED(!cu && t.size(0) == d.c.batch, "[batch, tokens, heads, d] rows are for uniform batches");
+  return {t.size(0) * t.size(1), 4, t.size(0), t.size(1)};
+}
+
+// t as rows of `heads` heads for these tokens.
+cca_rows_t rows_of(const Desc &d, const at::Tensor &t, const Tokens &n, int64_t heads) {
+  const int dt = dtype_of(t.scalar_type());
+  NEED(dt >= 0 && t.is_cuda() && t.get_device() == d.device,
+       "rows must be float32, bfloat16 or float16 and on the cache's device");
+  NEED(t.dim() == n.dims && t.size(0) == n.d0 && (n.dims == 3 || t.size(1) == n.d1) &&
+           t.size(-2) == heads,
+       "rows of " + std::to_string(heads) + " heads for the call's tokens expected");
+  NEED(t.size(-1) == d.c.head_dim && t.stride(-1) == 1,
+       "rows end in " + std::to_string(d.c.head_dim) + " contiguous channels");
+  cca_rows_t r;
+  r.ptr = t.data_ptr();
+  r.dtype = dt;
+  if (n.dims == 4) {
+    r.seq_stride = t.stride(0);
+    r.token_stride = t.stride(1);
+    r.head_stride = t.stride(2);
+  } else {
+    r.token_stride = t.stride(0);
+    r.head_stride = t.stride(1);
+    r.seq_stride = n.d0 / d.c.batch * r.token_stride;
+  }
+  return r;
+}
+
+const int *cu_of(const Desc &d, const at::Tensor *cu) {
+  if (!cu) return nullptr;
+  NEED(cu->scalar_type() == at::kInt && cu->is_cuda() && cu->get_device() == d.device &&
+           cu->numel() == d.c.batch + 1 && cu->is_contiguous(),
+       "cu_seqlens is a contiguous int32 tensor of batch + 1 on the cache's device");
+  return static_cast<const int *>(cu->data_ptr());
+}
+
+int count32(int64_t n) {
+  NEED(n < (int64_t(1) << 31), "too many tokens for one call");
+  return static_cast<int>(n);
+}
+
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType t, int device) {
+  return at::empty(shape, at::TensorOptions().dtype(t).device(at::kCUDA, device));
+}
+
+void *current_stream(int device) { return c10::cuda::getCurrentCUDAStream(device).stream(); }
+
+// Runs f, turning its exceptions into Python ones.
+template <typename F>
+PyObject *guarded(F f) {
+  try {
+    return f();
+  } catch (const Invalid &e) {
+    PyErr_SetString(PyExc_ValueError, e.what.c_str());
+  } catch (const std::exception &e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+bool arity(Py_ssize_t n, Py_ssize_t want) {
+  if (n == want) return true;
+  PyErr_Format(PyExc_TypeError, "%zd arguments expected, %zd given", want, n);
+  return false;
+}
+
+// describe(k, v, page_table, lengths, scales, status) -> bytes
+PyObject *describe(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  if (!arity(n, 6)) return nullptr;
+  return guarded([&]() -> PyObject * {
+    const at::Tensor *k = tensor(a[0], "k"), *v = tensor(a[1], "v"), *table = tensor(a[2], "page_table"),
+                     *len = tensor(a[3], "lengths"), *sc = tensor(a[4], "scales"), *st = tensor(a[5], "status");
+    NEED(k && v && table && len, "k, v, page_table and lengths are tensors");
+    NEED(k->dim() == 4 && v->sizes() == k->sizes() && v->scalar_type() == k->scalar_type(),
+         "k and v are [n_pages, n_kv_heads, page_size, row] of one type");
+    if (sc) {
+      NEED(k->scalar_type() == at::kByte, "pages of 4 bits are uint8");
+      NEED(sc->scalar_type() == at::kHalf && sc->dim() == 4 && sc->size(0) == k->size(0) &&
+               sc->size(1) == k->size(1) && sc->size(2) == k->size(2) && sc->size(3) == 4,
+           "scales are [n_pages, n_kv_heads, page_size, 4] float16");
+    } else {
+      NEED(k->scalar_type() == at::kHalf || k->scalar_type() == at::kBFloat16,
+           "pages of 16 bits are float16 or bfloat16");
+    }
+    NEED(table->dim() == 2 && len->dim() == 1 && len->size(0) == table->size(0) &&
+             table->scalar_type() == at::kInt && len->scalar_type() == at::kInt,
+         "page_table is int32 [batch, max_pages], lengths int32 [batch]");
+    NEED(!st || (st->scalar_type() == at::kInt && st->numel() >= 1), "status is an int32 tensor of one element");
+    const at::Device dev = k->device();
+    for (const at::Tensor *t : {k, v, table, len, sc, st})
+      NEED(!t || (t->device() == dev && t->is_contiguous()),
+           "the cache's tensors are contiguous and on one device");
+    for (int64_t s : {k->size(0), k->size(1), k->size(2), 2 * k->size(3), table->size(0), table->size(1)})
+      NEED(s < (int64_t(1) << 31), "a size of the cache is beyond 31 bits");
+    Desc d{};
+    d.c.k = k->data_ptr();
+    d.c.v = v->data_ptr();
+    d.c.scales = sc ? sc->data_ptr() : nullptr;
+    d.c.page_table = static_cast<const int *>(table->data_ptr());
+    d.c.lengths = static_cast<int *>(len->data_ptr());
+    d.c.status = st ? static_cast<int *>(st->data_ptr()) : nullptr;
+    d.c.batch = static_cast<int>(table->size(0));
+    d.c.max_pages = static_cast<int>(table->size(1));
+    d.c.n_pages = static_cast<int>(k->size(0));
+    d.c.page_size = static_cast<int>(k->size(2));
+    d.c.n_kv_heads = static_cast<int>(k->size(1));
+    d.c.head_dim = static_cast<int>(sc ? 2 * k->size(3) : k->size(3));
+    d.c.bits = sc ? 4 : 16;
+    d.c.dtype = sc ? CCA_F16 : dtype_of(k->scalar_type());
+    d.device = dev.is_cuda() ? dev.index() : -1;
+    return PyBytes_FromStringAndSize(reinterpret_cast<const char *>(&d), sizeof(d));
+  });
+}
+
+// append(desc, k, v, q, cu_seqlens, rope_base, q_out) -> q_out (None without q) or status
+PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  if (!arity(n, 7)) return nullptr;
+  return guarded([&]() -> PyObject * {
+    const Desc &d = desc_of(a[0]);
+    const at::Tensor *k = tensor(a[1], "k"), *v = tensor(a[2], "v"), *q = tensor(a[3], "q"),
+                     *cu = tensor(a[4], "cu_seqlens"), *qo = tensor(a[6], "q_out");
+    const double base = PyFloat_AsDouble(a[5]);
+    if (PyErr_Occurred()) return nullptr;
+    NEED(k && v, "k and v are tensors");
+    NEED(q || !qo, "q_out without q");
+    const int *cup = cu_of(d, cu);
+    const Tokens t = tokens_of(d, *k, cup);
+    const cca_rows_t kr = rows_of(d, *k, t, d.c.n_kv_heads), vr = rows_of(d, *v, t, d.c.n_kv_heads);
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(d.device));
+    cca_rows_t qr{}, qor{};
+    at::Tensor made;
+    int heads = 0;
+    if (q) {
+      NEED(q->dim() >= 2, "q is [tokens, heads, d] or [batch, tokens, heads, d]");
+      heads = count32(q->size(-2));
+      qr = rows_of(d, *q, t, heads);
+      if (!qo) {
+        made = fresh(q->sizes(), q->scalar_type(), d.device);
+        qo = &made;
+      }
+      qor = rows_of(d, *qo, t, heads);
+    }
+    const int rc = g_append(&d.c, q ? &qr : nullptr, &kr, &vr, q ? &qor : nullptr, heads, cup,
+                            count32(t.n), static_cast<float>(base), current_stream(d.device));
+    if (rc != CCA_OK) return PyLong_FromLong(rc);
+    if (made.defined()) return THPVariable_Wrap(made);
+    PyObject *r = q ? a[6] : Py_None;
+    Py_INCREF(r);
+    return r;
+  });
+}
+
+// attend(desc, q, cu_seqlens, scale, out) -> out or status
+PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  if (!arity(n, 5)) return nullptr;
+  return guarded([&]() -> PyObject * {
+    const Desc &d = desc_of(a[0]);
+    const at::Tensor *q = tensor(a[1], "q"), *cu = tensor(a[2], "cu_seqlens"), *out = tensor(a[4], "out");
+    const double scale = PyFloat_AsDouble(a[3]);
+    if (PyErr_Occurred()) return nullptr;
+    NEED(q, "q is a tensor");
+    const int *cup = cu_of(d, cu);
+    const Tokens t = tokens_of(d, *q, cup);
+    const int heads = count32(q->size(-2)), tokens = count32(t.n);
+    const cca_rows_t qr = rows_of(d, *q, t, heads);
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(d.device));
+    at::Tensor made;
+    if (!out) {
+      made = fresh(q->sizes(), q->scalar_type(), d.device);
+      out = &made;
+    }
+    const cca_rows_t o = rows_of(d, *out, t, heads);
+    // scratch of its own for every call: captured graphs and streams never share one
+    const size_t bytes = g_attention_ws(&d.c, heads, tokens);
+    const at::Tensor ws = fresh({static_cast<int64_t>(bytes)}, at::kByte, d.device);
+    const int rc = g_attention(&d.c, &qr, &o, heads, cup, tokens, static_cast<float>(scale),
+                               ws.data_ptr(), bytes, current_stream(d.device));
+    if (rc != CCA_OK) return PyLong_FromLong(rc);
+    if (made.defined()) return THPVariable_Wrap(made);
+    Py_INCREF(a[4]);
+    return a[4];
+  });
+}
+
+// gather(desc, k_out, v_out, cu_seqlens) -> None or status
+PyObject *gather(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  if (!arity(n, 4)) return nullptr;
+  return guarded([&]() -> PyObject * {
+    const Desc &d = desc_of(a[0]);
+    const at::Tensor *k = tensor(a[1], "k_out"), *v = tensor(a[2], "v_out"), *cu = tensor(a[3], "cu_seqlens");
+    NEED(k && v, "k_out and v_out are tensors");
+    const int *cup = cu_of(d, cu);
+    const Tokens t = tokens_of(d, *k, cup);
+    const cca_rows_t kr = rows_of(d, *k, t, d.c.n_kv_heads), vr = rows_of(d, *v, t, d.c.n_kv_heads);
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(d.device));
+    const int rc = g_gather(&d.c, &kr, &vr, cup, count32(t.n), current_stream(d.device));
+    if (rc != CCA_OK) return PyLong_FromLong(rc);
+    Py_RETURN_NONE;
+  });
+}
+
+// bind(append, gather, attention, attention_workspace_size): the entry points' addresses
+PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  if (!arity(n, 4)) return nullptr;
+  void *p[4];
+  for (int i = 0; i < 4; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
+  if (PyErr_Occurred()) return nullptr;
+  g_append = reinterpret_cast<decltype(g_append)>(p[0]);
+  g_gather = reinterpret_cast<decltype(g_gather)>(p[1]);
+  g_attention = reinterpret_cast<decltype(g_attention)>(p[2]);
+  g_attention_ws = reinterpret_cast<decltype(g_attention_ws)>(p[3]);
+  Py_RETURN_NONE;
+}
+
+template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
+PyMethodDef method(const char *name) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
+}
+
+PyMethodDef methods[] = {method<bind>("bind"),     method<describe>("describe"),
+                         method<append>("append"), method<attend>("attend"),
+                         method<gather>("gather"), {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_bind", nullptr, -1, methods,
+                      nullptr,               nullptr,       nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__paged_bind(void) { return PyModule_Create(&module); }

@@ -4,14 +4,30 @@ memory and marshals arguments only."""
 from __future__ import annotations
 
 import contextlib
+import ctypes
 
 import torch
 
-from . import (CCA_BF16, CCA_F16, CCA_F32, cca_paged_append, cca_paged_attention,
-               cca_paged_attention_workspace_size, cca_paged_cache_t, cca_paged_check,
-               cca_paged_gather, cca_rows_t)
+from . import _check, cca_paged_cache_t, cca_paged_check, load
 
-_DTYPES = {torch.float32: CCA_F32, torch.bfloat16: CCA_BF16, torch.float16: CCA_F16}
+_bind = None
+
+
+def _native():
+    """The native marshalling (csrc/paged_bind.cpp), bound to the loaded library's entry points."""
+    global _bind
+    if _bind is None:
+        lib = load()
+        try:
+            from . import _paged_bind
+        except ImportError as e:
+            raise RuntimeError("_paged_bind.so is missing: build it with "
+                               "`python -m compressed_latent_space_b200.build`") from e
+        names = ("cca_paged_append", "cca_paged_gather", "cca_paged_attention",
+                 "cca_paged_attention_workspace_size")
+        _paged_bind.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
+        _bind = _paged_bind
+    return _bind
 
 
 class PagedCache:
@@ -40,7 +56,7 @@ class PagedCache:
         if n_pages is None:
             table.copy_(torch.arange(pages, dtype=torch.int32).view(batch, max_pages))
         lengths = torch.zeros(batch, dtype=torch.int32, device=device)
-        self._take(k, v, table, lengths, scales)
+        self._take(k, v, table, lengths, scales, torch.zeros(1, dtype=torch.int32, device=device))
 
     @classmethod
     def from_pages(cls, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
@@ -50,79 +66,51 @@ class PagedCache:
         float16 or bfloat16, or [.., head_dim / 2] uint8 with ``scales`` [.., page_size, 4]
         float16; ``status`` an int32 of one element (None: kernel-side errors go unrecorded)."""
         self = cls.__new__(cls)
-        self._take(k, v, page_table, lengths, scales, status, own_status=False)
+        self._take(k, v, page_table, lengths, scales, status)
         return self
 
-    def _take(self, k, v, table, lengths, scales, status=None, own_status=True):
+    def _take(self, k, v, table, lengths, scales, status):
+        self._call = bind = _native()
+        self._desc = bind.describe(k, v, table, lengths, scales, status)
         self.device = k.device
-        self.bits = 16 if scales is None else 4
-        if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
-            raise ValueError("k and v are [n_pages, n_kv_heads, page_size, row] of one type")
-        if (k.dtype != torch.uint8) if self.bits == 4 else (k.dtype not in (torch.float16, torch.bfloat16)):
-            raise ValueError(f"pages of {self.bits} bits cannot be {k.dtype}")
-        n_pages, n_kv, page_size, row = k.shape
-        if scales is not None and (scales.shape != (n_pages, n_kv, page_size, 4)
-                                   or scales.dtype != torch.float16):
-            raise ValueError("scales are [n_pages, n_kv_heads, page_size, 4] float16")
-        if (table.dim() != 2 or lengths.shape != table.shape[:1] or table.dtype != torch.int32
-                or lengths.dtype != torch.int32):
-            raise ValueError("page_table is int32 [batch, max_pages], lengths int32 [batch]")
-        if own_status:
-            status = torch.zeros(1, dtype=torch.int32, device=self.device)
-        if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
-            raise ValueError("status is an int32 tensor of one element")
-        for t in (k, v, table, lengths, scales, status):
-            if t is not None and (t.device != self.device or not t.is_contiguous()):
-                raise ValueError("the cache's tensors are contiguous and on one device")
         self.k, self.v, self.scales = k, v, scales
         self.page_table, self.lengths, self.status = table, lengths, status
-        self.batch, self.max_pages = table.shape
-        self.n_kv_heads, self.page_size = n_kv, page_size
-        self.head_dim = row * 2 if self.bits == 4 else row
-        self.struct = cca_paged_cache_t(
-            k.data_ptr(), v.data_ptr(), None if scales is None else scales.data_ptr(),
-            table.data_ptr(), lengths.data_ptr(), None if status is None else status.data_ptr(),
-            self.batch, self.max_pages, n_pages, page_size, n_kv, self.head_dim, self.bits,
-            CCA_F16 if self.bits == 4 else _DTYPES[k.dtype])
         self.conv_state = self.vshift_state = None     # a layer's (CCALayer.new_paged_cache)
 
-    # ------------------------------------------------------------------ marshalling
+    @property
+    def struct(self) -> cca_paged_cache_t:
+        """The cache as the C ABI takes it."""
+        return cca_paged_cache_t.from_buffer_copy(self._desc)
+
+    @property
+    def bits(self) -> int:
+        return 16 if self.scales is None else 4
+
+    @property
+    def batch(self) -> int:
+        return self.page_table.shape[0]
+
+    @property
+    def max_pages(self) -> int:
+        return self.page_table.shape[1]
+
+    @property
+    def page_size(self) -> int:
+        return self.k.shape[2]
+
+    @property
+    def n_kv_heads(self) -> int:
+        return self.k.shape[1]
+
+    @property
+    def head_dim(self) -> int:
+        return self.k.shape[3] * (1 if self.scales is None else 2)
+
     def _on(self, stream):
-        """The device and, where given, the stream that the call's allocations belong to."""
+        """The device and, where given, the stream that a call's allocations belong to."""
         if stream is not None:
             return torch.cuda.stream(stream)
-        if torch.cuda.current_device() == self.device.index:
-            return contextlib.nullcontext()
         return torch.cuda.device(self.device)
-
-    def _tokens(self, t: torch.Tensor, cu) -> int:
-        if t.dim() == 4:
-            if cu is not None or t.shape[0] != self.batch:
-                raise ValueError("[batch, tokens, heads, d] rows are for uniform batches")
-            return t.shape[0] * t.shape[1]
-        if t.dim() != 3:
-            raise ValueError("rows are [tokens, heads, d] or [batch, tokens, heads, d]")
-        return t.shape[0]
-
-    def _rows(self, t: torch.Tensor, like=None, heads: int | None = None) -> cca_rows_t:
-        if t.device != self.device or t.dtype not in _DTYPES:
-            raise ValueError(f"rows must be floating and on {self.device}")
-        if t.shape[-1] != self.head_dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
-            raise ValueError(f"rows end in {self.head_dim} contiguous channels")
-        if heads is not None and t.shape[-2] != heads:
-            raise ValueError(f"{t.shape[-2]} heads, {heads} expected")
-        if like is not None and t.shape[:-2] != like.shape[:-2]:
-            raise ValueError(f"rows of {tuple(t.shape[:-2])} tokens beside {tuple(like.shape[:-2])}")
-        if t.dim() == 4:
-            return cca_rows_t(t.data_ptr(), _DTYPES[t.dtype], t.stride(0), t.stride(1), t.stride(2))
-        per = t.shape[0] // self.batch
-        return cca_rows_t(t.data_ptr(), _DTYPES[t.dtype], per * t.stride(0), t.stride(0), t.stride(1))
-
-    def _cu(self, cu):
-        if cu is not None and (cu.dtype != torch.int32 or cu.device != self.device
-                               or cu.numel() != self.batch + 1 or not cu.is_contiguous()):
-            raise ValueError("cu_seqlens is a contiguous int32 tensor of batch + 1 on the cache's device")
-        return cu
 
     # ------------------------------------------------------------------ the operators
     def append(self, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor | None = None,
@@ -130,38 +118,29 @@ class PagedCache:
                q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
         """Stores the new tokens' keys and values in their pages; with rope_base > 1 keys and
         queries are rotated to their positions on the way.  Returns the rotated queries."""
-        cu = self._cu(cu_seqlens)
-        n = self._tokens(k, cu)
-        kr, vr = self._rows(k, None, self.n_kv_heads), self._rows(v, k, self.n_kv_heads)
-        with self._on(stream):
-            qr = qo = None
-            if q is not None:
-                qr = self._rows(q, k)
-                if q_out is None:
-                    q_out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-                qo = self._rows(q_out, k, q.shape[-2])
-            cca_paged_append(self.struct, qr, kr, vr, qo, q.shape[-2] if q is not None else 0, cu, n,
-                             rope_base, stream)
-        return q_out if q is not None else None
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.append(k, v, q, cu_seqlens, rope_base, q_out)
+        r = self._call.append(self._desc, k, v, q, cu_seqlens, rope_base, q_out)
+        if type(r) is int:
+            _check(r)
+        return r
 
     def attend(self, q: torch.Tensor, cu_seqlens: torch.Tensor | None = None,
                scale: float | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Causal attention of the new tokens' queries over their sequences' pages (which hold
         the new tokens already); scale None: 1 / sqrt(head_dim)."""
-        cu = self._cu(cu_seqlens)
-        n, heads = self._tokens(q, cu), q.shape[-2]
-        if scale is not None and scale == 0.0:
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.attend(q, cu_seqlens, scale, out)
+        if scale is None:
+            scale = 0.0
+        elif scale == 0.0:
             raise ValueError("a scale of 0 is not taken (None means 1 / sqrt(head_dim))")
-        qr = self._rows(q)
-        with self._on(stream):
-            if out is None:
-                out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-            orow = self._rows(out, q, heads)
-            # scratch of its own for every call: captured graphs and streams never share one
-            ws = torch.empty(cca_paged_attention_workspace_size(self.struct, heads, n),
-                             dtype=torch.uint8, device=self.device)
-            cca_paged_attention(self.struct, qr, orow, heads, cu, n, scale or 0.0, ws, stream)
-        return out
+        r = self._call.attend(self._desc, q, cu_seqlens, scale, out)
+        if type(r) is int:
+            _check(r)
+        return r
 
     def gather(self, tokens: int | None = None, cu_seqlens: torch.Tensor | None = None,
                k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
@@ -169,15 +148,16 @@ class PagedCache:
         """The cached rows, dense: (k, v) of [tokens, n_kv_heads, d] with room for sequence b at
         cu_seqlens[b], or the given outputs (uniform rows of any strides; packed with
         cu_seqlens).  Rows behind a sequence's end are left as they are."""
-        cu = self._cu(cu_seqlens)
-        with self._on(stream):
-            if k_out is None:
-                dt = dtype or (torch.float16 if self.bits == 4 else self.k.dtype)
-                shape = (tokens, self.n_kv_heads, self.head_dim)
-                k_out, v_out = (torch.empty(shape, dtype=dt, device=self.device) for _ in range(2))
-            n = self._tokens(k_out, cu)
-            cca_paged_gather(self.struct, self._rows(k_out, None, self.n_kv_heads),
-                             self._rows(v_out, k_out, self.n_kv_heads), cu, n, stream)
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.gather(tokens, cu_seqlens, k_out, v_out, dtype)
+        if k_out is None:
+            dt = dtype or (torch.float16 if self.scales is not None else self.k.dtype)
+            k_out, v_out = torch.empty((2, tokens, self.n_kv_heads, self.head_dim), dtype=dt,
+                                       device=self.device).unbind(0)
+        r = self._call.gather(self._desc, k_out, v_out, cu_seqlens)
+        if type(r) is int:
+            _check(r)
         return k_out, v_out
 
     def check(self, stream=None):
