@@ -29,9 +29,10 @@
 // second product's operand.
 //
 // Softmax: running maximum per row, moved only when a score passes it by more than 8 (in log2
-// units), so p <= 2^8; sums in float32.  4 bits: p vs is rounded to float16 after a power of two
-// nrm (per warp, following the largest vs met) has brought vs under 2^7: 11 bits of each weight
-// whatever the values' scale.  16-bit pages: p itself in float16, or, for bfloat16 pages, as two
+// units), so p <= 2^8; sums in float32.  4 bits: p vs is rounded to float16, for which a power of
+// two 2^e (per warp, following the largest vs met) brings vs under 2^7: 11 bits of each weight
+// whatever the values' scale.  2^e rides in the maximum (m holds the maximum less e), so that p,
+// its sum and all it weighs carry it, and it cancels.  16-bit pages: p itself in float16, or, for bfloat16 pages, as two
 // bfloat16 terms (one would keep 8 bits).  q . n: the queries in float16 times a power of two
 // that brings the warp's largest to 2^14 (exact but for elements 2^28 below it).
 //
@@ -65,7 +66,9 @@ FastDiv fast_div(uint32_t d) {
 __device__ __forceinline__ int div(int x, const FastDiv &f) {
   return static_cast<int>((__umulhi(static_cast<uint32_t>(x), f.mul) + static_cast<uint32_t>(x)) >> f.shift);
 }
-// x / d for x >= 0 and a quotient below 2^22, rd = 1 / d: the float quotient is off by one at most.
+// x / d for x >= 0 and a quotient below 2^20, rd = 1 / d to 2 ulp: the float quotient is off by one
+// at most.
+__device__ __forceinline__ float rcp(int d) { return __fdividef(1.f, __int2float_rn(d)); }
 __device__ __forceinline__ int div(int x, int d, float rd) {
   int q = __float2int_rz(__int2float_rn(x) * rd);
   const int r = x - q * d;
@@ -87,7 +90,7 @@ struct AttnParams {
   float *part_o;                 // [2 CTAs][R][D]
   float2 *part_ml;               // [2 CTAs][R]
   int max_pages, n_pages, page_log2, Hkv, G, warps;
-  FastDiv by_g, by_hkv;
+  FastDiv by_g, by_hkv, by_warps;
   int whole;                     // > 0: items are never split, none has more tiles than this
   float scale_log2;
 };
@@ -168,6 +171,21 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
+// d = a b, without an accumulator to clear first
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16_zero(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -217,12 +235,13 @@ struct Core {
   float ksf;                     // factor of a raw score into log2 units
   float m[NT][2], l[NT][2], z[NT][2];
   float o[MT][NT][4];
-  float nrm;
+  float vlim;                    // 2^(7 - e)
+  float vexp;                    // e of the value scales (4 bits)
   bool first;                    // no tile yet: m is not a maximum
 
-  __device__ __forceinline__ void mma_qk(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-    if constexpr (BF_QK) mma_bf16_16816(d, a, b);
-    else mma_f16_16816(d, a, b);
+  __device__ __forceinline__ void mma_qk(bool zero, float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    if constexpr (BF_QK) zero ? mma_bf16_zero(d, a, b) : mma_bf16_16816(d, a, b);
+    else zero ? mma_f16_zero(d, a, b) : mma_f16_16816(d, a, b);
   }
 
   // the row of a tile that column `col` of n-tile nt belongs to
@@ -326,7 +345,8 @@ struct Core {
   }
 
   __device__ __forceinline__ void reset() {
-    nrm = __uint_as_float(227u << 23);               // 2^100: the first scale met brings it down
+    vexp = BITS == 4 ? 40.f : 0.f;                   // the first scale met brings it down
+    vlim = __uint_as_float((127u + 7 - 40) << 23);   // (float16 scales are 2^-24 and more, or 0)
     first = true;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -472,10 +492,6 @@ struct Core {
     float c[SF][NT][4];
     float2 vzs[SF][2];                               // (scale, zero) of the lane's values
     float top = -INFINITY, vtop = 0.f;
-#pragma unroll
-    for (int f = 0; f < SF; ++f)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) c[f][nt][0] = c[f][nt][1] = c[f][nt][2] = c[f][nt][3] = 0.f;
     if constexpr (LDSM) {
 #pragma unroll
       for (int blk = 0; blk < S::KB; blk += BPL) {
@@ -488,7 +504,7 @@ struct Core {
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_qk(c[(blk + i) / X][nt], a[ks], qf[(blk + i) % X][nt][ks]);
+            for (int nt = 0; nt < NT; ++nt) mma_qk((blk + i) % X == 0 && ks == 0, c[(blk + i) / X][nt], a[ks], qf[(blk + i) % X][nt][ks]);
         }
       }
     } else {
@@ -499,7 +515,7 @@ struct Core {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_qk(c[blk / X][nt], a[ks], qf[blk % X][nt][ks]);
+          for (int nt = 0; nt < NT; ++nt) mma_qk(blk % X == 0 && ks == 0, c[blk / X][nt], a[ks], qf[blk % X][nt][ks]);
       }
     }
 #pragma unroll
@@ -537,7 +553,8 @@ struct Core {
         }
       }
     }
-    if (__any_sync(0xffffffffu, first || top > kLazy || (BITS == 4 && vtop * nrm > 128.f))) raise(c, vtop);
+    // (2^7 >= vtop 2^vexp as vtop <= 2^(7 - vexp))
+    if (__any_sync(0xffffffffu, first || top > kLazy + vexp || (BITS == 4 && vtop > vlim))) raise(c, vtop);
     uint32_t pb[SF][NT][2], pl[SF][NT][2];
 #pragma unroll
     for (int f = 0; f < SF; ++f) {
@@ -552,9 +569,9 @@ struct Core {
           uint64_t acc = add2(f2(l[nt][0], l[nt][1]), p2);
           unf2(acc, l[nt][0], l[nt][1]);
           if constexpr (BITS == 4) {
-            const float vn = vzs[f][half].x * nrm, vz = vzs[f][half].y;
+            const float vs = vzs[f][half].x, vz = vzs[f][half].y;
             float w0, w1, z0, z1;
-            unf2(mul2(p2, f2(vn, vn)), w0, w1);
+            unf2(mul2(p2, f2(vs, vs)), w0, w1);
             unf2(fma2(p2, f2(vz, vz), f2(z[nt][0], z[nt][1])), z0, z1);
             if (MASK) {                              // a masked key's scale may be anything
               if (x0 == -INFINITY) { w0 = 0.f; z0 = z[nt][0]; }
@@ -618,9 +635,21 @@ struct Core {
     }
   }
 
-  // New running maxima (scores c, less the old ones, are taken down with them) and, 4 bits, a new
-  // power of two of the value scales.
+  // New running maxima and, 4 bits, a new power of two of the value scales (scores c, less the old
+  // m, become less the new).
   __device__ __forceinline__ void raise(float (&c)[SF][NT][4], float vtop) {
+    float e = vexp;
+    if constexpr (BITS == 4) {
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
+      if (vtop > vlim) {
+        // 2^6 <= vtop 2^e < 2^7 (an infinite scale, which only rows that see it may notice, as the
+        // largest finite one)
+        const int x = min(15, static_cast<int>((__float_as_uint(vtop) >> 23) & 255u) - 127);
+        e = static_cast<float>(6 - x);
+        vlim = __uint_as_float(static_cast<uint32_t>(7 - (6 - x) + 127) << 23);
+      }
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -632,8 +661,10 @@ struct Core {
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
         const float old = m[nt][col];
-        // (a row without a visible key keeps m and its sums of zero)
-        const float now = mx == -INFINITY ? old : (first ? old + mx : fmaxf(old, old + mx));
+        // the score maximum: old + vexp before, old + mx of this tile (a row without a visible
+        // key keeps its own, with sums of zero)
+        float now = first ? old + mx : fmaxf(old + vexp, old + mx);
+        now = (mx == -INFINITY ? old + vexp : now) - e;
         const float al = first ? 0.f : ex2(old - now);
         m[nt][col] = now;
         l[nt][col] *= al;
@@ -649,23 +680,8 @@ struct Core {
           c[f][nt][2 + col] = (c[f][nt][2 + col] + old) - now;
         }
       }
+    vexp = e;
     first = false;
-    if constexpr (BITS == 4) {
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
-      if (vtop * nrm > 128.f) {
-        const int e = static_cast<int>((__float_as_uint(vtop) >> 23) & 255u) - 127;
-        const float nn = __uint_as_float(static_cast<uint32_t>(6 - e + 127) << 23);
-        const float f = nn / nrm;
-        nrm = nn;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e4 = 0; e4 < 4; ++e4) o[mt][nt][e4] *= f;
-      }
-    }
   }
 
   // l and z over the lanes of a row; o in the values' units, the zeros' share added; the column
@@ -681,7 +697,7 @@ struct Core {
           if constexpr (BITS == 4) z[nt][e] += __shfl_xor_sync(0xffffffffu, z[nt][e], off);
         }
     if constexpr (BITS == 4) {
-      const float f0 = 16777216.f / nrm, f1 = 1048576.f / nrm;
+      constexpr float f0 = 16777216.f, f1 = 1048576.f;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -810,14 +826,14 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
     const bool few = !p.whole && 2 * items <= p.warps;
     if (p.whole) {
       pad = p.whole;
-      upw = pad * ((items + p.warps - 1) / p.warps);
+      upw = pad * div(items + p.warps - 1, p.by_warps);
     } else {
       const int w = p.warps - (few ? items * 5 / 8 : 0);
-      upw = max(1, (tiles + w - 1) / w);
+      upw = max(1, div(tiles + w - 1, w, rcp(w)));
       pad = few ? upw : 1;
     }
     for (int attempt = 0;; ++attempt) {
-      const float rpad = 1.f / pad;
+      const float rpad = rcp(pad);
       int sum = 0;
       for (int b = b0; b < b1; ++b) {
         if (per > 1) mine = paged_seq(p.batch, b, nullptr);
@@ -845,7 +861,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
       }
       if (attempt == 0 && few && all > static_cast<long long>(upw) * p.warps) {
         const int w = p.warps - items;
-        pad = upw = max(1, (tiles + w - 1) / w);
+        pad = upw = max(1, div(tiles + w - 1, w, rcp(w)));
         continue;
       }
       if (tid == 0) pre[0] = 0;
@@ -864,7 +880,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
       }
     }
   }
-  const float rpad = 1.f / pad;
+  const float rpad = rcp(pad);
   const int total = pre[B];
   const int w = blockIdx.x * kWarps + warp;
   int u = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(w) * upw));
@@ -874,19 +890,17 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
   C core;
 
   while (u < uend) {
-    int b;
-    {
-      int lo = 0, hi = B;                            // the last b with pre[b] <= u
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (pre[mid] <= u) lo = mid;
-        else hi = mid;
-      }
-      b = lo;
+    int b = 0;                                       // the last one with pre[b] <= u
+    for (int first = 0, n = B; n > 0;) {             // lanes probe [first, first + n) at 32 places
+      const int each = (n + 31) >> 5, i = first + lane * each;
+      const unsigned below = __ballot_sync(0xffffffffu, i < first + n && pre[min(i, B)] <= u);
+      first += (31 - __clz(below)) * each;           // (pre[first] <= u always)
+      n = each == 1 ? 0 : min(each, B - first);
+      b = first;
     }
     const PagedSeq s = paged_seq(p.batch, b, nullptr);
     const int per_head = div(pre[b + 1] - pre[b], p.by_hkv);
-    const int h = div(u - pre[b], per_head, 1.f / per_head);
+    const int h = div(u - pre[b], per_head, rcp(per_head));
     int t0 = u - pre[b] - h * per_head, rt = 0, T, TP;
     while (true) {
       T = tiles_of(s, rt, R, p.by_g, KTL);
@@ -904,26 +918,32 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
     // of the first tiles (and of the next one later, a tile ahead of its copies)
     typename C::Raw qraw;
     C::load_q(p, s, b, h, r0, rows, g, t, qraw);
-    auto look = [&](int i) {                         // lane kb < KB: first row of block kb, or -1
-      const int key = i * KT + lane * 16;
+    // lane j holds the first row (-1: none) of the run's 16-key block 32 n + j, for two n: looked
+    // up 32 blocks at a time, a batch ahead of the copies
+    const int blk0 = t0 * S::KB;
+    auto look = [&](int n) {
+      const int blk = blk0 + n * 32 + lane, key = blk * 16;
       int row = -1;
-      if (lane < S::KB && i < t1 && key < s.len) {
+      if (blk < t1 * S::KB && key < s.len) {
         const int page = paged_page(p.table, p.max_pages, p.n_pages, b, key >> p.page_log2, p.status);
         if (page >= 0)
           row = ((page * p.Hkv + h) << p.page_log2) + (key & ((1 << p.page_log2) - 1));
       }
       return row;
     };
-    int ahead[kStages];
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) ahead[i] = look(t0 + i);
-    int next = ahead[kStages - 1];
-    auto copy = [&](int i, int slot, int rows16) {
+    int rows_now = look(0), rows_next = look(1);
+    int looked = 1, at_blk = 0;                      // the next copy's first block within the batch
+    auto copy = [&](int i, int slot) {
       if (i < t1) {
+        if (at_blk == 32) {
+          at_blk = 0;
+          rows_now = rows_next;
+          rows_next = look(++looked);
+        }
         uint8_t *kd = ring_p + slot * S::TILE, *vd = kd + KT * ROWB, *sd = vd + KT * ROWB;
         const int sdst = BITS == 4 ? lane ^ (((lane >> 3) & 1) << 2) : 0;   // scale_at, in 16 bytes
         if (p.page_log2 >= KTL) {                    // the tile is one run of rows of a page
-          const int row = __shfl_sync(0xffffffffu, rows16, 0);
+          const int row = __shfl_sync(0xffffffffu, rows_now, at_blk);
           const uint8_t *ks = p.k + static_cast<size_t>(max(row, 0)) * ROWB + lane * 16;
           const uint8_t *vs = p.v + static_cast<size_t>(max(row, 0)) * ROWB + lane * 16;
 #pragma unroll
@@ -944,7 +964,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
 #pragma unroll
           for (int j = 0; j < KT * ROWB / 512; ++j) {
             const int cidx = j * 32 + lane, blk = cidx / ROWB, cb = cidx % ROWB;
-            const int row = __shfl_sync(0xffffffffu, rows16, blk);
+            const int row = __shfl_sync(0xffffffffu, rows_now, at_blk + blk);
             bool ok = row >= 0;
             int dst = BITS == 4 && D >= 32 ? piece4<D>(cidx / (D / 32), cidx % (D / 32)) : cidx;
             if constexpr (BITS == 16) {
@@ -956,17 +976,18 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
             cp_async16_zfill(vd + dst * 16, p.v + src, ok);
           }
           if constexpr (BITS == 4) {
-            const int row = __shfl_sync(0xffffffffu, rows16, lane >> 3);
+            const int row = __shfl_sync(0xffffffffu, rows_now, at_blk + (lane >> 3));
             cp_async16_zfill(sd + sdst * 16, p.scales + static_cast<size_t>(max(row, 0)) + (lane & 7) * 2,
                              row >= 0);
           }
         }
+        at_blk += S::KB;
       }
       cp_async_commit();
     };
     __syncwarp();                                    // the ring's last readers are done
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) copy(t0 + i, i, ahead[i]);
+    for (int i = 0; i < kStages - 1; ++i) copy(t0 + i, i);
 
     core.reset();
     core.set_q(p, qraw, g, t);
@@ -984,9 +1005,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
     for (int i = t0; i < t1; ++i) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();
-      const int rows16 = next;
-      next = look(i + kStages);
-      copy(i + kStages - 1, slot == 0 ? kStages - 1 : slot - 1, rows16);
+      copy(i + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
       const uint32_t kb = ring + slot * S::TILE, vb = kb + KT * ROWB, sb = vb + KT * ROWB;
       if ((i + 1) * KT <= first_lim) core.template tile<false>(kb, vb, sb, i * KT, lim, s.len, lane);
       else core.template tile<true>(kb, vb, sb, i * KT, lim, s.len, lane);
@@ -1104,7 +1123,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
   const int p0 = p.plan[b], p1 = p.plan[b + 1], upw = p.plan[p.batch.B + 1], pad = p.plan[p.batch.B + 2];
   const int rows = s.n * p.G, rts = row_tiles(s, R, p.G);
   if (rr >= rows) return;
-  const float rpad = 1.f / pad;
+  const float rpad = rcp(pad);
   int u0 = p0 + h * div(p1 - p0, p.by_hkv);
   for (int rt = 0; rt < rts; ++rt) {
     const int T = tiles_of(s, rt, R, p.by_g, KTL);
@@ -1303,6 +1322,7 @@ cudaError_t paged_attention(const PagedArgs &a, cudaStream_t st) {
   p.G = a.H / a.Hkv;
   p.by_g = fast_div(p.G);
   p.by_hkv = fast_div(a.Hkv);
+  p.by_warps = fast_div(static_cast<uint32_t>(ctas * kWarps));
   p.warps = ctas * kWarps;
   p.scale_log2 = static_cast<float>(a.scale * 1.4426950408889634);
   switch (a.D) {
