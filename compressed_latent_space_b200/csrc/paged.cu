@@ -25,16 +25,89 @@ struct AppendParams {
   const int *table;
   int *status;
   int max_pages, n_pages, page_log2, Hkv, HQ, page_f16;
+  int rpt, groups;               // rows of a thread, threads' row groups of a token
+  FastDiv by_tokens;
   bool rotate;
   float turn_hi[64], turn_lo[64];   // RoPE frequencies in turns, hi + lo (rope_turns_host)
 };
 
-// One thread takes channels [8 l, 8 l + 8) and their rotation partners d/2 above of one
-// (token, head) row, so a row is D / 16 neighbouring lanes: 16-byte loads of 16-bit inputs, the
-// rotation inside the thread, and the extremes of a 4-bit row over at most 8 lanes.
-// HQ query heads (rotated into qo), then Hkv keys, then Hkv values per token.
-template <int D, int BITS>
-__global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ AppendParams p) {
+// Eight consecutive elements of a row as loaded, and as floats.
+struct Raw8 {
+  uint4 a, b;                    // b: the upper four of float32
+  __device__ __forceinline__ void load(const void *ptr, size_t off, int dtype) {
+    if (dtype == CCA_F32) {
+      const float *f = static_cast<const float *>(ptr) + off;
+      a = *reinterpret_cast<const uint4 *>(f);
+      b = *reinterpret_cast<const uint4 *>(f + 4);
+    } else {
+      a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(ptr) + off);
+    }
+  }
+  __device__ __forceinline__ void get(int dtype, float (&o)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    if (dtype == CCA_F32) {
+      const uint32_t u[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[i] = __uint_as_float(w[i]);
+        o[4 + i] = __uint_as_float(u[i]);
+      }
+    } else if (dtype == CCA_F16) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        o[2 * i] = f.x;
+        o[2 * i + 1] = f.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[2 * i] = __uint_as_float(w[i] << 16);
+        o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  }
+};
+
+// The codes of eight elements at zero z and scale sc > 0, element e in bits 4 e ..: the quotient
+// by a reciprocal, good to 15 2^-22, and where that leaves a rounding open (within 1e-5 of a half)
+// by the division itself.
+__device__ __forceinline__ uint32_t codes4(const float (&x)[8], float z, float sc) {
+  const float inv = __fdividef(1.f, sc);
+  constexpr float kMagic = 12582912.f;               // 1.5 2^23: the sum's low bits are the integer
+  uint32_t w = 0;
+  bool open = false;
+#pragma unroll
+  for (int e = 7; e >= 0; --e) {
+    const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[e], z), inv), 0.f), 15.f);
+    const float s = __fadd_rn(q, kMagic);
+    open = open || fabsf(q - (s - kMagic)) > 0.49999f;
+    w = w * 16u + __float_as_uint(s);
+  }
+  w -= 0x4b400000u * 0x11111111u;                    // the exponents, added at every digit
+  if (open) {
+    w = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float n = rintf(__fdiv_rn(__fsub_rn(x[e], z), sc));
+      w |= static_cast<uint32_t>(fminf(fmaxf(n, 0.f), 15.f)) << (4 * e);
+    }
+  }
+  return w;
+}
+
+// One thread takes channels [8 l, 8 l + 8) and their rotation partners d/2 above of `rpt`
+// consecutive rows of one token (HQ query heads, rotated into qo, then Hkv keys, then Hkv values):
+// 16-byte loads of 16-bit inputs, the next row's asked for before this one is worked on, the
+// rotation inside the thread with one set of angles for all its rows, and the extremes of a 4-bit
+// row over the at most 8 neighbouring lanes that share it.  Neighbouring lanes take neighbouring
+// tokens at the same rows: no warp mixes queries, keys and values (their paths differ), and a
+// head's new slots of a page are written in one piece.  rpt is 1 until the threads fill the
+// machine: a prompt's cost is instructions, most of them angles and addresses, a step's is latency.
+// DT: the one element type of q, k, v, q_out and 16-bit pages, or -1 where they differ or are
+// float32 (the branches on five types cost as many instructions as the work).
+template <int D, int BITS, int DT>
+__global__ void __launch_bounds__(256, 4) paged_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LPR = D / 16, HALF = D / 2;
   __shared__ float thi[HALF], tlo[HALF];
   for (int i = threadIdx.x; i < HALF; i += blockDim.x) {
@@ -44,18 +117,16 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
   __syncthreads();
   pdl_launch_dependents();
   pdl_wait();
-  const int heads = p.HQ + 2 * p.Hkv;
-  const long long rows = static_cast<long long>(p.batch.tokens) * heads;
-  const long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const long long row = idx / LPR;
-  const int c0 = static_cast<int>(idx % LPR) * 8;
-  bool live = row < rows;
-  const int token = live ? static_cast<int>(row / heads) : 0;
-  const int hh = live ? static_cast<int>(row % heads) : 0;
+  const int heads = p.HQ + 2 * p.Hkv, kv0 = p.HQ + p.Hkv;
+  const int idx = blockIdx.x * blockDim.x + threadIdx.x;       // below 2^28 (the call's limit)
+  const int c0 = idx % LPR * 8, unit = idx / LPR;
+  const int group = div(unit, p.by_tokens), token = unit - group * p.batch.tokens;
+  int row = group * p.rpt;
+  bool live = group < p.groups;
   // the token's sequence: the last b with cu[b] <= token
   const bool packed = p.batch.cu != nullptr;
-  int b;
-  if (packed) {
+  int b = 0;
+  if (live && packed) {
     int lo = 0, hi = p.batch.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -63,112 +134,141 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
       else hi = mid;
     }
     b = lo;
-  } else {
-    b = token / (p.batch.tokens / p.batch.B);
+  } else if (live) {
+    b = div(token, p.batch.by_n);
   }
   const PagedSeq s = paged_seq(p.batch, b, p.status);
   const int i = token - s.t0;
   const int pos = s.len - s.n + i;
   live = live && i >= 0 && i < s.n && pos >= 0 && s.len > 0;
-
-  const bool is_q = hh < p.HQ, is_k = !is_q && hh < p.HQ + p.Hkv;
-  const int h = is_q ? hh : (is_k ? hh - p.HQ : hh - p.HQ - p.Hkv);
-  float lo8[8], hi8[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) lo8[j] = hi8[j] = 0.f;
-  if (live) {
-    const Rows &src = is_q ? p.q : (is_k ? p.nk : p.nv);
-    const size_t off = row_offset(src, packed, s, b, i, h) + c0;
-    load8_as(src.ptr, off, src.dtype, lo8);
-    load8_as(src.ptr, off + HALF, src.dtype, hi8);
-    if (p.rotate && (is_q || is_k)) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float c, sn;
-        rope_cos_sin_turns(pos, thi[c0 + j], tlo[c0 + j], c, sn);
-        const float a = lo8[j], bb = hi8[j];
-        lo8[j] = a * c - bb * sn;
-        hi8[j] = a * sn + bb * c;
-      }
+  // this thread's place in the token's first q, k, v and q_out rows
+  const size_t q0 = row_offset(p.q, packed, s, b, i, 0) + c0, k0 = row_offset(p.nk, packed, s, b, i, 0) + c0,
+               v0 = row_offset(p.nv, packed, s, b, i, 0) + c0, o0 = row_offset(p.qo, packed, s, b, i, 0) + c0;
+  const int end = min(heads, row + p.rpt);
+  Raw8 lo_raw, hi_raw;
+  auto ask = [&](int r) {
+    if (!live || r >= end) return;
+    if (r < p.HQ) {
+      const size_t off = q0 + static_cast<size_t>(r) * static_cast<uint32_t>(p.q.head);
+      lo_raw.load(p.q.ptr, off, DT >= 0 ? DT : p.q.dtype);
+      hi_raw.load(p.q.ptr, off + HALF, DT >= 0 ? DT : p.q.dtype);
+    } else {
+      const Rows &src = r < kv0 ? p.nk : p.nv;
+      const size_t off = (r < kv0 ? k0 : v0) + static_cast<size_t>(r < kv0 ? r - p.HQ : r - kv0) * static_cast<uint32_t>(src.head);
+      lo_raw.load(src.ptr, off, DT >= 0 ? DT : src.dtype);
+      hi_raw.load(src.ptr, off + HALF, DT >= 0 ? DT : src.dtype);
     }
+  };
+  ask(row);
+  size_t slot0 = 0;                                  // the token's slot in its page, head 0
+  bool store = false;
+  if (live && end > p.HQ) {
+    const int page = paged_page(p.table, p.max_pages, p.n_pages, b, pos >> p.page_log2, p.status);
+    store = page >= 0;
+    slot0 = ((static_cast<size_t>(max(page, 0)) * p.Hkv) << p.page_log2) + (pos & ((1 << p.page_log2) - 1));
   }
-  if (is_q) {
-    if (live) {
-      const size_t off = row_offset(p.qo, packed, s, b, i, h) + c0;
-      store8_as(p.qo.ptr, off, p.qo.dtype, lo8);
-      store8_as(p.qo.ptr, off + HALF, p.qo.dtype, hi8);
-    }
+  float cs[8], sn[8];
+  if (p.rotate && row < kv0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rope_cos_sin_turns(pos, thi[c0 + j], tlo[c0 + j], cs[j], sn[j]);
   }
-  int page = -1;
-  if (live && !is_q)
-    page = paged_page(p.table, p.max_pages, p.n_pages, b, pos >> p.page_log2, p.status);
-  const size_t slot =
-      ((static_cast<size_t>(page < 0 ? 0 : page) * p.Hkv + h) << p.page_log2) + (pos & ((1 << p.page_log2) - 1));
-  if constexpr (BITS == 16) {
-    if (page >= 0) {
-      uint8_t *pages = is_k ? p.k : p.v;
-      const int dt = p.page_f16 ? CCA_F16 : CCA_BF16;
-      if (p.page_f16) {
-        float m = 0.f;                               // a NaN or a value beyond float16
-        bool bad = false;
+  // (rpt is the same for all lanes: they leave the loop together)
+#pragma unroll 1
+  for (int j = 0; j < p.rpt; ++j, ++row) {
+    const bool is_q = row < p.HQ, is_k = !is_q && row < kv0, on = live && row < end;
+    float lo8[8], hi8[8];
+    if (on) {
+      const int in_dtype = DT >= 0 ? DT : (is_q ? p.q.dtype : (is_k ? p.nk.dtype : p.nv.dtype));
+      lo_raw.get(in_dtype, lo8);
+      hi_raw.get(in_dtype, hi8);
+    } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          m = fmaxf(m, fmaxf(fabsf(lo8[j]), fabsf(hi8[j])));
-          bad = bad || isnan(lo8[j]) || isnan(hi8[j]);
-        }
-        if (bad || m > kF16Max) report(p.status, DEV_RANGE);
+      for (int e = 0; e < 8; ++e) lo8[e] = hi8[e] = 0.f;
+    }
+    ask(row + 1);
+    if (on && p.rotate && row < kv0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = lo8[e], y = hi8[e];
+        lo8[e] = x * cs[e] - y * sn[e];
+        hi8[e] = x * sn[e] + y * cs[e];
       }
-      store8_as(pages, slot * D + c0, dt, lo8);
-      store8_as(pages, slot * D + c0 + HALF, dt, hi8);
     }
-  } else {
-    float mn = lo8[0], mx = lo8[0], nan = 0.f;       // nan: 0, or NaN when an element is not finite
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      mn = fminf(mn, fminf(lo8[j], hi8[j]));
-      mx = fmaxf(mx, fmaxf(lo8[j], hi8[j]));
-      nan += __fmul_rn(lo8[j], 0.f) + __fmul_rn(hi8[j], 0.f);
-    }
-#pragma unroll
-    for (int off = 1; off < LPR; off <<= 1) {
-      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      nan += __shfl_xor_sync(0xffffffffu, nan, off);
-    }
-    __half zh = __float2half_rn(mn);
-    __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.f));
-    const bool bad = nan != 0.f || __hisinf(zh) || __hisinf(sh);
-    if (bad) {                                       // the whole vector reads back as NaN
-      zh = __ushort_as_half(0x7fff);
-      sh = __ushort_as_half(0x7fff);
-    }
-    const float z = __half2float(zh), sc = __half2float(sh);
-    if (page >= 0) {
-      if (bad) report(p.status, DEV_RANGE);
-      uint32_t wl = 0, wh = 0;
-      if (!bad && sc > 0.f) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float nl = rintf(__fdiv_rn(__fsub_rn(lo8[j], z), sc));
-          const float nh = rintf(__fdiv_rn(__fsub_rn(hi8[j], z), sc));
-          wl |= static_cast<uint32_t>(fminf(fmaxf(nl, 0.f), 15.f)) << (4 * j);
-          wh |= static_cast<uint32_t>(fminf(fmaxf(nh, 0.f), 15.f)) << (4 * j);
-        }
+    if (is_q) {
+      if (on) {
+        const size_t off = o0 + static_cast<size_t>(row) * static_cast<uint32_t>(p.qo.head);
+        store8_as(p.qo.ptr, off, DT >= 0 ? DT : p.qo.dtype, lo8);
+        store8_as(p.qo.ptr, off + HALF, DT >= 0 ? DT : p.qo.dtype, hi8);
       }
-      uint8_t *dst = (is_k ? p.k : p.v) + slot * (D / 2) + c0 / 2;
-      *reinterpret_cast<uint32_t *>(dst) = wl;
-      *reinterpret_cast<uint32_t *>(dst + HALF / 2) = wh;
-      if (c0 == 0) p.scales[slot * 2 + (is_k ? 0 : 1)] = __halves2half2(sh, zh);
+      if (BITS == 16) continue;                      // (4 bits: other lanes may share in the extremes)
+    }
+    const int h = is_k ? row - p.HQ : row - kv0;
+    const size_t slot = slot0 + (static_cast<size_t>(max(h, 0)) << p.page_log2);
+    if constexpr (BITS == 16) {
+      if (on && store) {
+        uint8_t *pages = is_k ? p.k : p.v;
+        const int dt = DT >= 0 ? DT : (p.page_f16 ? CCA_F16 : CCA_BF16);
+        if (dt == CCA_F16) {
+          float top = 0.f, sum = 0.f;                // the sum is NaN where an element is
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            top = max3(top, fabsf(lo8[e]), fabsf(hi8[e]));
+            sum += fabsf(lo8[e]) + fabsf(hi8[e]);
+          }
+          if (top > kF16Max || isnan(sum)) report(p.status, DEV_RANGE);
+        }
+        store8_as(pages, slot * D + c0, dt, lo8);
+        store8_as(pages, slot * D + c0 + HALF, dt, hi8);
+      }
+    } else {
+      float mn = lo8[0], mx = lo8[0], sum = 0.f;     // sum of magnitudes: finite where all are
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        mn = fminf(mn, fminf(lo8[e], hi8[e]));
+        mx = max3(mx, lo8[e], hi8[e]);
+        sum += fabsf(lo8[e]) + fabsf(hi8[e]);
+      }
+#pragma unroll
+      for (int off = 1; off < LPR; off <<= 1) {
+        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      }
+      if (on && !is_q && store) {
+        __half zh = __float2half_rn(mn);
+        __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.f));
+        // (a sum beyond float32 has an element beyond float16)
+        const bool bad = !isfinite(sum) || __hisinf(zh) || __hisinf(sh);
+        if (bad) {                                   // the whole vector reads back as NaN
+          zh = __ushort_as_half(0x7fff);
+          sh = __ushort_as_half(0x7fff);
+          report(p.status, DEV_RANGE);
+        }
+        const float z = __half2float(zh), sc = __half2float(sh);
+        uint32_t wl = 0, wh = 0;
+        if (!bad && sc > 0.f) {
+          wl = codes4(lo8, z, sc);
+          wh = codes4(hi8, z, sc);
+        }
+        uint8_t *dst = (is_k ? p.k : p.v) + slot * (D / 2) + c0 / 2;
+        *reinterpret_cast<uint32_t *>(dst) = wl;
+        *reinterpret_cast<uint32_t *>(dst + HALF / 2) = wh;
+        if (c0 == 0) p.scales[slot * 2 + (is_k ? 0 : 1)] = __halves2half2(sh, zh);
+      }
     }
   }
 }
 
 template <int D, int BITS>
 cudaError_t launch_append(const PagedArgs &a, const AppendParams &p, cudaStream_t st) {
-  const long long threads = static_cast<long long>(a.tokens) * (p.HQ + 2 * a.Hkv) * (D / 16);
-  const long long blocks = (threads + 255) / 256;
-  return launch_pdl(paged_append_kernel<D, BITS>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                    st, p);
+  const long long threads = static_cast<long long>(a.tokens) * p.groups * (D / 16);
+  const dim3 grid(static_cast<unsigned>((threads + 255) / 256)), block(256);
+  const int dt = a.nk.dtype;
+  const bool same = a.nv.dtype == dt && (!p.HQ || (a.q.dtype == dt && a.qo.dtype == dt)) &&
+                    (a.bits == 4 || (dt == CCA_F16) == (a.page_f16 != 0));
+  if (same && dt == CCA_F16) return launch_pdl(paged_append_kernel<D, BITS, CCA_F16>, grid, block, 0, st, p);
+  if (same && dt == CCA_BF16) return launch_pdl(paged_append_kernel<D, BITS, CCA_BF16>, grid, block, 0, st, p);
+  return launch_pdl(paged_append_kernel<D, BITS, -1>, grid, block, 0, st, p);
 }
 
 // ------------------------------------------------------------------ gather
@@ -180,46 +280,60 @@ struct GatherParams {
   const int *table;
   int *status;
   int max_pages, n_pages, page_log2, Hkv, page_f16;
+  FastDiv by_rows;               // 2 Hkv
 };
 
-// Eight channels of one (token, head, key or value) per thread; the CTAs of sequence blockIdx.y
-// walk its tokens in strides, so the grid needs no length.
+// Sixteen channels of one (token, head, key or value) per thread and step; the CTAs of sequence
+// blockIdx.y walk its rows in strides, so the grid needs no length.
 template <int D, int BITS>
 __global__ void __launch_bounds__(256) paged_gather_kernel(const __grid_constant__ GatherParams p) {
-  constexpr int CPR = D / 8;
+  constexpr int CPR = D / 16;
   const int b = blockIdx.y;
   pdl_launch_dependents();
   pdl_wait();
   const PagedSeq s = paged_seq(p.batch, b, p.status);
   const bool packed = p.batch.cu != nullptr;
   const int n = min(s.len, s.n);
-  const int per_token = 2 * p.Hkv * CPR;
-  const long long total = static_cast<long long>(n) * per_token;
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long e = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; e < total;
-       e += stride) {
-    const int i = static_cast<int>(e / per_token), r = static_cast<int>(e % per_token);
-    const int which = r / (p.Hkv * CPR), h = r / CPR % p.Hkv, c0 = r % CPR * 8;
+  const int total = n * (2 * p.Hkv) * CPR;           // below 2^28 (the call's limit)
+  const int stride = gridDim.x * blockDim.x;
+#pragma unroll 4
+  for (int e = blockIdx.x * blockDim.x + threadIdx.x; e < total; e += stride) {
+    const int c0 = e % CPR * 16, row = e / CPR;
+    const int i = div(row, p.by_rows), r = row - i * (2 * p.Hkv);
+    const int which = r >= p.Hkv, h = which ? r - p.Hkv : r;
     const int page = paged_page(p.table, p.max_pages, p.n_pages, b, i >> p.page_log2, p.status);
-    float v8[8];
+    const Rows &dst = which ? p.nv : p.nk;
+    const size_t off = row_offset(dst, packed, s, b, i, h) + c0;
+    const size_t slot = ((static_cast<size_t>(max(page, 0)) * p.Hkv + h) << p.page_log2) +
+                        (i & ((1 << p.page_log2) - 1));
+    const uint8_t *pages = which ? p.v : p.k;
+    float x[8], y[8];
+    if (page < 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v8[j] = 0.f;
-    if (page >= 0) {
-      const size_t slot = ((static_cast<size_t>(page) * p.Hkv + h) << p.page_log2) +
-                          (i & ((1 << p.page_log2) - 1));
-      const uint8_t *pages = which ? p.v : p.k;
-      if constexpr (BITS == 16) {
-        load8_as(pages, slot * D + c0, p.page_f16 ? CCA_F16 : CCA_BF16, v8);
-      } else {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(pages + slot * (D / 2) + c0 / 2);
-        const float2 sz = __half22float2(p.scales[slot * 2 + which]);
+      for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.f;
+    } else if constexpr (BITS == 16) {
+      const int dt = p.page_f16 ? CCA_F16 : CCA_BF16;
+      if (dst.dtype == dt) {                         // moved as it is
+        const uint4 *from = reinterpret_cast<const uint4 *>(pages + (slot * D + c0) * 2);
+        uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(dst.ptr) + off);
+        const uint4 u = from[0], v = from[1];
+        to[0] = u;
+        to[1] = v;
+        continue;
+      }
+      load8_as(pages, slot * D + c0, dt, x);
+      load8_as(pages, slot * D + c0 + 8, dt, y);
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2 *>(pages + slot * (D / 2) + c0 / 2);
+      const float2 sz = __half22float2(p.scales[slot * 2 + which]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          v8[j] = __fadd_rn(__fmul_rn(static_cast<float>((w >> (4 * j)) & 15u), sz.x), sz.y);
+      for (int j = 0; j < 8; ++j) {
+        x[j] = __fadd_rn(__fmul_rn(static_cast<float>((w.x >> (4 * j)) & 15u), sz.x), sz.y);
+        y[j] = __fadd_rn(__fmul_rn(static_cast<float>((w.y >> (4 * j)) & 15u), sz.x), sz.y);
       }
     }
-    const Rows &dst = which ? p.nv : p.nk;
-    store8_as(dst.ptr, row_offset(dst, packed, s, b, i, h) + c0, dst.dtype, v8);
+    store8_as(dst.ptr, off, dst.dtype, x);
+    store8_as(dst.ptr, off + 8, dst.dtype, y);
   }
 }
 
@@ -227,21 +341,10 @@ template <int D, int BITS>
 cudaError_t launch_gather(const PagedArgs &a, const GatherParams &p, cudaStream_t st) {
   // enough CTAs of a sequence to cover its share of the rows, at most 8 per SM in all
   const long long per_seq = (static_cast<long long>(a.tokens) + a.B - 1) / a.B;
-  const long long want = (per_seq * 2 * a.Hkv * (D / 8) + 255) / 256;
+  const long long want = (per_seq * 2 * a.Hkv * (D / 16) + 255) / 256;
   const long long most = 8LL * num_sms() / a.B + 1;
   const unsigned gx = static_cast<unsigned>(want < most ? (want < 1 ? 1 : want) : most);
   return launch_pdl(paged_gather_kernel<D, BITS>, dim3(gx, a.B), dim3(256), 0, st, p);
-}
-
-PagedBatch batch_of(const PagedArgs &a) {
-  PagedBatch b;
-  b.lengths = a.lengths;
-  b.cu = a.cu;
-  b.B = a.B;
-  b.tokens = a.tokens;
-  b.len_add = a.len_add;
-  b.cap = a.max_pages << a.page_log2;
-  return b;
 }
 
 }  // namespace
@@ -249,7 +352,7 @@ PagedBatch batch_of(const PagedArgs &a) {
 cudaError_t paged_append(const PagedArgs &a, cudaStream_t st) {
   if (a.tokens == 0) return cudaSuccess;
   AppendParams p;
-  p.batch = batch_of(a);
+  p.batch = paged_batch(a);
   p.q = a.q;
   p.qo = a.qo;
   p.nk = a.nk;
@@ -265,6 +368,11 @@ cudaError_t paged_append(const PagedArgs &a, cudaStream_t st) {
   p.Hkv = a.Hkv;
   p.HQ = a.q.ptr ? a.H : 0;
   p.page_f16 = a.page_f16;
+  const int heads = p.HQ + 2 * a.Hkv;
+  const long long want = static_cast<long long>(a.tokens) * heads * (a.D / 16) / (2048LL * num_sms());
+  p.rpt = static_cast<int>(want < 1 ? 1 : (want < heads ? want : heads));
+  p.groups = (heads + p.rpt - 1) / p.rpt;
+  p.by_tokens = fast_div(static_cast<uint32_t>(a.tokens));
   p.rotate = a.rope_base > 0.f;
   rope_turns_host(a.D, p.rotate ? a.rope_base : 2.0, p.turn_hi, p.turn_lo, 64);
 #define CCA_APPEND(DD)                                                                  \
@@ -281,7 +389,7 @@ cudaError_t paged_append(const PagedArgs &a, cudaStream_t st) {
 cudaError_t paged_gather(const PagedArgs &a, cudaStream_t st) {
   if (a.tokens == 0) return cudaSuccess;
   GatherParams p;
-  p.batch = batch_of(a);
+  p.batch = paged_batch(a);
   p.nk = a.nk;
   p.nv = a.nv;
   p.k = static_cast<const uint8_t *>(a.k);
@@ -294,6 +402,7 @@ cudaError_t paged_gather(const PagedArgs &a, cudaStream_t st) {
   p.page_log2 = a.page_log2;
   p.Hkv = a.Hkv;
   p.page_f16 = a.page_f16;
+  p.by_rows = fast_div(static_cast<uint32_t>(2 * a.Hkv));
 #define CCA_GATHER(DD)                                                                  \
   if (a.D == DD)                                                                        \
     return a.bits == 4 ? launch_gather<DD, 4>(a, p, st) : launch_gather<DD, 16>(a, p, st);

@@ -8,12 +8,40 @@
 
 namespace cca {
 
+// Division of 0 <= x < 2^31 by a divisor that the host knows (Granlund and Montgomery 1994).
+struct FastDiv {
+  uint32_t mul, shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f;
+  f.shift = 0;
+  while ((1ull << f.shift) < d) ++f.shift;
+  f.mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << f.shift) - d)) / d + 1);
+  return f;
+}
+__device__ __forceinline__ int div(int x, const FastDiv &f) {
+  return static_cast<int>((__umulhi(static_cast<uint32_t>(x), f.mul) + static_cast<uint32_t>(x)) >> f.shift);
+}
+
 // The batch as the kernels see it: how many tokens sequence b holds (len, the call's new ones
 // included), how many of them are new (n), and where its new rows start (t0: packed row index).
 struct PagedBatch {
   const int *lengths, *cu;
   int B, tokens, len_add, cap;
+  FastDiv by_n;                  // a uniform batch's new tokens per sequence
 };
+
+inline PagedBatch paged_batch(const PagedArgs &a) {
+  PagedBatch b;
+  b.lengths = a.lengths;
+  b.cu = a.cu;
+  b.B = a.B;
+  b.tokens = a.tokens;
+  b.len_add = a.len_add;
+  b.cap = a.max_pages << a.page_log2;
+  b.by_n = fast_div(a.cu || a.tokens < a.B ? 1 : a.tokens / a.B);
+  return b;
+}
 
 struct PagedSeq {
   int len, n, t0;

@@ -64,6 +64,8 @@ int check_rows(const cca::PagedArgs &a, const char *name, const cca_rows_t *r, i
     return fail(CCA_ERR_ALIGNMENT, "%s: pointer and strides must be multiples of 16 bytes", name);
   if (r->token_stride < 0 || r->head_stride < 0 || (!a.cu && r->seq_stride < 0))
     return fail(CCA_ERR_INVALID_ARG, "%s has a negative stride", name);
+  if (r->token_stride >= (1LL << 31) || r->head_stride >= (1LL << 31))
+    return fail(CCA_ERR_UNSUPPORTED, "%s: token and head strides must stay below 2^31", name);
   const int n = a.cu ? a.tokens : a.tokens / a.B;
   if (output && ((n > 1 && r->token_stride < a.D) || (heads > 1 && r->head_stride < a.D) ||
                  (!a.cu && a.B > 1 && r->seq_stride < a.D)))
