@@ -50,6 +50,10 @@ size_t paged_attention_workspace(const PagedArgs &a);
 // counts them in 32 bits.
 long long paged_attention_units(const PagedArgs &a);
 cudaError_t paged_attention(const PagedArgs &a, cudaStream_t st);
+// The kernel for many rows a sequence behind it (4 bits), on `ctas` CTAs; params: its AttnParams.
+int paged_tc_rows();
+int paged_tc_keys();
+cudaError_t paged_attention_tc(const PagedArgs &a, const void *params, int ctas, cudaStream_t st);
 
 
 // The layer's decode step over a paged cache (decode.cu): a holds x, y, the weights, the states,

@@ -43,43 +43,15 @@
 // middle to begin another item.  A run that covers an item writes its rows; pieces that meet in
 // a CTA are joined there, the rest (at most two per CTA) go through the workspace to the merge
 // kernel, always added in order, so results do not depend on timing.
-#include "paged.cuh"
+#include "paged_attention.cuh"
 
 namespace cca {
 namespace {
 
 constexpr int kWarps = 4;        // warps per CTA
 constexpr int kStages = 2;       // tiles per warp's ring (three or four measured the same at 4 bits, 2 % more at 16)
+constexpr long long kTcMinRows = 112;
 constexpr float kLazy = 8.f;     // the running maximum moves when a score passes it by this much
-
-// x / d for x >= 0 and a quotient below 2^20, rd = 1 / d to 2 ulp: the float quotient is off by one
-// at most.
-__device__ __forceinline__ float rcp(int d) { return __fdividef(1.f, __int2float_rn(d)); }
-__device__ __forceinline__ int div(int x, int d, float rd) {
-  int q = __float2int_rz(__int2float_rn(x) * rd);
-  const int r = x - q * d;
-  if (r < 0) --q;
-  else if (r >= d) ++q;
-  return q;
-}
-
-struct AttnParams {
-  PagedBatch batch;
-  Rows q, o;
-  __nv_bfloat16 *o_lo;           // with o.dtype == kRowsSplit
-  const uint8_t *k, *v;
-  const uint2 *scales;
-  const int *table;
-  int *status;
-  int *plan;                     // [B + 3]: units before each sequence, run length, item padding
-  float *spill;                  // [warps][R D + 2 R]
-  float *part_o;                 // [2 CTAs][R][D]
-  float2 *part_ml;               // [2 CTAs][R]
-  int max_pages, n_pages, page_log2, Hkv, G, warps;
-  FastDiv by_g, by_hkv, by_warps;
-  int whole;                     // > 0: items are never split, none has more tiles than this
-  float scale_log2;
-};
 
 template <int D, int BITS>
 struct Shape {
@@ -172,32 +144,6 @@ __device__ __forceinline__ void mma_bf16_zero(float (&d)[4], const uint32_t (&a)
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Tiles of keys that the rows of row tile rt see; one even where there is none, so that some
-// warp writes the rows.
-__device__ __forceinline__ int tiles_of(const PagedSeq &s, int rt, int R, const FastDiv &by_g, int kt_log2) {
-  const int last = min(s.n - 1, div(rt * R + R - 1, by_g));
-  const int keys = max(0, min(s.len, s.len - s.n + last + 1));
-  return max(1, (keys + (1 << kt_log2) - 1) >> kt_log2);
-}
-__device__ __forceinline__ int row_tiles(const PagedSeq &s, int R, int G) {
-  return (s.n * G + R - 1) / R;
-}
-// Units of an item on the line.
-__device__ __forceinline__ int padded(int tiles, int pad, float rpad) {
-  return div(tiles + pad - 1, pad, rpad) * pad;
-}
-// Where row r of (sequence b, head h) goes in the output.
-__device__ __forceinline__ size_t out_offset(const AttnParams &p, const PagedSeq &s, int b, int h, int r) {
-  const int tok = div(r, p.by_g);
-  return row_offset(p.o, p.batch.cu != nullptr, s, b, tok, h * p.G + r - tok * p.G);
-}
-
 // RW rows per tile.  Up to 8 rows share one 8-column product; with RW = 4 or 2 the columns are
 // split among X = 8 / RW blocks of 16 keys (block x's products run against queries that are zero
 // outside columns [x RW, (x + 1) RW), so X of them add up in one accumulator without touching
@@ -716,51 +662,12 @@ struct Core {
   }
 };
 
-// N consecutive output channels of one row
-template <int N>
-__device__ __forceinline__ void store_row(const Rows &o, __nv_bfloat16 *o_lo, size_t off,
-                                          const float (&v)[N]) {
-  if (o.dtype == CCA_F32) {
-    float *d = static_cast<float *>(o.ptr) + off;
-#pragma unroll
-    for (int i = 0; i < N; i += 2) *reinterpret_cast<float2 *>(d + i) = make_float2(v[i], v[i + 1]);
-  } else if (o.dtype == CCA_F16) {
-    uint32_t *d = reinterpret_cast<uint32_t *>(static_cast<__half *>(o.ptr) + off);
-#pragma unroll
-    for (int i = 0; i < N; i += 2) d[i / 2] = pack_f16x2(v[i], v[i + 1]);
-  } else {
-    uint32_t *d = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(o.ptr) + off);
-    uint32_t *dl = reinterpret_cast<uint32_t *>(o_lo + off);
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      uint32_t hi, lo;
-      split_bf16x2(make_float2(v[i], v[i + 1]), hi, lo);
-      d[i / 2] = hi;
-      if (o.dtype == kRowsSplit) dl[i / 2] = lo;
-    }
-  }
-}
-
 // What a warp's run left of an item it did not cover.
 enum : int { kNone = 0, kOpen = 1, kEnds = 2 };      // kEnds: the piece has the item's last tile
 struct PieceAt {
   int state, b, h, rt;
   const float *at;               // [R][D] sums, [R][2] maximum and sum
 };
-
-// (m, l, acc) joined with another piece of the same row.  A piece without a visible key has l = 0
-// and no maximum.
-__device__ __forceinline__ void join(float &m, float &l, float4 &acc, float m2, float l2, const float4 &v) {
-  if (l2 == 0.f) return;
-  const float mn = l == 0.f ? m2 : fmaxf(m, m2);
-  const float fa = l == 0.f ? 0.f : ex2(m - mn), fb = ex2(m2 - mn);
-  m = mn;
-  l = l * fa + l2 * fb;
-  acc.x = acc.x * fa + v.x * fb;
-  acc.y = acc.y * fa + v.y * fb;
-  acc.z = acc.z * fa + v.z * fb;
-  acc.w = acc.w * fa + v.w * fb;
-}
 
 template <int D, int BITS, int R, bool QBF16, bool PBF16>
 __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_attention_kernel(const __grid_constant__ AttnParams p) {
@@ -790,7 +697,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
       mine = paged_seq(p.batch, b, p.status);
       const int rts = row_tiles(mine, R, p.G);
       items += rts;
-      for (int rt = 0; rt < rts; ++rt) tiles += tiles_of(mine, rt, R, p.by_g, KTL);
+      for (int rt = 0; rt < rts; ++rt) tiles += tiles_of<KT>(mine, rt, R, p.by_g);
     }
     const int wt = __reduce_add_sync(0xffffffffu, tiles), wi = __reduce_add_sync(0xffffffffu, items);
     if (lane == 0) {
@@ -825,7 +732,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
         if (per > 1) mine = paged_seq(p.batch, b, nullptr);
         const int rts = row_tiles(mine, R, p.G);
         int u = 0;
-        for (int rt = 0; rt < rts; ++rt) u += padded(tiles_of(mine, rt, R, p.by_g, KTL), pad, rpad);
+        for (int rt = 0; rt < rts; ++rt) u += padded(tiles_of<KT>(mine, rt, R, p.by_g), pad, rpad);
         u *= p.Hkv;
         pre[b + 1] = u;
         sum += u;
@@ -889,7 +796,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
     const int h = div(u - pre[b], per_head, rcp(per_head));
     int t0 = u - pre[b] - h * per_head, rt = 0, T, TP;
     while (true) {
-      T = tiles_of(s, rt, R, p.by_g, KTL);
+      T = tiles_of<KT>(s, rt, R, p.by_g);
       TP = padded(T, pad, rpad);
       if (t0 < TP) break;
       t0 -= TP;
@@ -1090,80 +997,6 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
   }
 }
 
-// Joins the pieces of the items that more than one CTA worked on: WPR warps per (row of a tile,
-// head, sequence).  D / 4 lanes hold the row's channels; the lane groups take pieces in turn and
-// are added in a fixed order.
-template <int D, int R, int KTL, int WPR>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ AttnParams p, int rows_max) {
-  constexpr int LN = D / 4, GW = 32 / LN, GR = GW * WPR, UN = 4;   // UN pieces in flight per group
-  __shared__ float so[WPR == 4 ? 4 : 1][D];
-  __shared__ float2 sml[4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit = WPR == 4 ? blockIdx.x : blockIdx.x * 4 + warp;
-  const int h = unit / rows_max, rr = unit - h * rows_max, b = blockIdx.y;
-  const int ln = lane % LN, grp = (WPR == 4 ? warp * GW : 0) + lane / LN;
-  pdl_launch_dependents();
-  pdl_wait();
-  if (h >= p.Hkv) return;
-  const PagedSeq s = paged_seq(p.batch, b, nullptr);
-  const int p0 = p.plan[b], p1 = p.plan[b + 1], upw = p.plan[p.batch.B + 1], pad = p.plan[p.batch.B + 2];
-  const int rows = s.n * p.G, rts = row_tiles(s, R, p.G);
-  if (rr >= rows) return;
-  const float rpad = rcp(pad);
-  int u0 = p0 + h * div(p1 - p0, p.by_hkv);
-  for (int rt = 0; rt < rts; ++rt) {
-    const int T = tiles_of(s, rt, R, p.by_g, KTL);
-    const int ca = u0 / upw / kWarps, cz = (u0 + T - 1) / upw / kWarps, r = rt * R + rr;
-    u0 += padded(T, pad, rpad);
-    if (ca == cz || r >= rows) continue;
-    float m = 0.f, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c0 = ca + grp; c0 <= cz; c0 += UN * GR) {
-      float2 ml[UN];
-      float4 v[UN];
-#pragma unroll
-      for (int i = 0; i < UN; ++i) {
-        const int c = c0 + i * GR;
-        const size_t at = (static_cast<size_t>(min(c, cz)) * 2 + (c == ca ? 1 : 0)) * R + rr;
-        ml[i] = c <= cz ? p.part_ml[at] : make_float2(0.f, 0.f);
-        v[i] = c <= cz ? *reinterpret_cast<const float4 *>(p.part_o + at * D + ln * 4)
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int i = 0; i < UN; ++i) join(m, l, acc, ml[i].x, ml[i].y, v[i]);
-    }
-    __syncwarp();
-#pragma unroll
-    for (int off = LN; off < 32; off <<= 1) {        // the warp's groups, lower first
-      const float m2 = __shfl_down_sync(0xffffffffu, m, off), l2 = __shfl_down_sync(0xffffffffu, l, off);
-      float4 v;
-      v.x = __shfl_down_sync(0xffffffffu, acc.x, off);
-      v.y = __shfl_down_sync(0xffffffffu, acc.y, off);
-      v.z = __shfl_down_sync(0xffffffffu, acc.z, off);
-      v.w = __shfl_down_sync(0xffffffffu, acc.w, off);
-      join(m, l, acc, m2, l2, v);
-    }
-    if constexpr (WPR == 4) {
-      __syncthreads();
-      if (lane < LN) *reinterpret_cast<float4 *>(&so[warp][ln * 4]) = acc;
-      if (lane == 0) sml[warp] = make_float2(m, l);
-      __syncthreads();
-      if (warp == 0 && lane < LN)
-#pragma unroll
-        for (int i = 1; i < 4; ++i)
-          join(m, l, acc, sml[i].x, sml[i].y, *reinterpret_cast<const float4 *>(&so[i][ln * 4]));
-    }
-    if ((WPR == 1 || warp == 0) && lane < LN) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const float v[4] = {l == 0.f ? 0.f : acc.x * inv, l == 0.f ? 0.f : acc.y * inv,
-                          l == 0.f ? 0.f : acc.z * inv, l == 0.f ? 0.f : acc.w * inv};
-      store_row<4>(p.o, p.o_lo, out_offset(p, s, b, h, r) + ln * 4, v);
-    }
-  }
-}
-
-inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
 // Rows of a tile, by the rows of an average sequence: a tile's keys are read and unpacked once
 // for all its rows, and a 4-bit tile of fewer than 8 rows scores several key blocks at a time.
 // 16 at most at d~ = 128, where 32 rows' accumulators would not fit the registers.
@@ -1174,6 +1007,15 @@ int pick_rows(const PagedArgs &a) {
   if (per <= 8) return 8;
   if (per <= 16 || a.D == 128) return 16;
   return 32;
+}
+
+// Where an average sequence has many rows, 4-bit attention runs on the 5th-generation tensor cores
+// (paged_attention_tc.cu).  Both measured, us a call, mma.sync / tcgen05: 2 x 8192 keys of 4 heads,
+// d~ = 64: 64 rows 20.9 / 23.0, 128 rows 28.9 / 24.0; 8 x 4096 of 16, d~ = 32: 96 rows 51.8 / 55.8,
+// 128 rows 61.0 / 58.1; 4 x 4096 of 4, d~ = 128: 64 rows 26.2 / 32.8, 128 rows 37.5 / 35.0.
+bool use_tc(const PagedArgs &a) {
+  const long long per = static_cast<long long>(a.tokens) / a.B * (a.H / a.Hkv);
+  return a.bits == 4 && a.D >= 32 && per >= kTcMinRows;
 }
 
 int key_tile_log2(const PagedArgs &a) {
@@ -1197,6 +1039,7 @@ int whole_tiles(const PagedArgs &a) {
 }
 
 int plan_ctas(const PagedArgs &a) {
+  if (use_tc(a)) return num_sms();
   long long per_sm = (227 * 1024) / static_cast<long long>(attn_smem(a) + 2048);
   const int by_regs = ctas_by_regs(a.D, a.bits, pick_rows(a));
   if (per_sm > by_regs) per_sm = by_regs;
@@ -1212,12 +1055,13 @@ struct AttnLayout {
 };
 AttnLayout attn_layout(const PagedArgs &a, int ctas) {
   AttnLayout L;
-  const size_t rows = static_cast<size_t>(ctas) * 2 * pick_rows(a);
+  const bool tc = use_tc(a);
+  const size_t rows = static_cast<size_t>(ctas) * 2 * (tc ? paged_tc_rows() : pick_rows(a));
   L.plan = 0;
   L.ml = align256(static_cast<size_t>(a.B + 3) * 4);
   L.o = L.ml + align256(rows * 8);
   L.spill = L.o + align256(rows * a.D * 4);
-  L.total = L.spill + align256(static_cast<size_t>(ctas) * kWarps * pick_rows(a) * (a.D + 2) * 4);
+  L.total = L.spill + (tc ? 0 : align256(static_cast<size_t>(ctas) * kWarps * pick_rows(a) * (a.D + 2) * 4));
   return L;
 }
 
@@ -1233,11 +1077,11 @@ cudaError_t launch(const PagedArgs &a, const AttnParams &p, int ctas, cudaStream
   const long long rows = static_cast<long long>(a.cu ? a.tokens : a.tokens / a.B) * p.G;
   const int rm = static_cast<int>(rows < R ? rows : R);
   // few rows have many pieces each: a CTA a row, else a warp
-  constexpr int KTL = Shape<D, BITS>::KTL;
+  constexpr int KT = Shape<D, BITS>::KT;
   const long long units = static_cast<long long>(rm) * a.Hkv;
   if (units * a.B <= 4LL * num_sms())
-    return launch_pdl(paged_merge_kernel<D, R, KTL, 4>, dim3(static_cast<unsigned>(units), a.B), dim3(128), 0, st, p, rm);
-  return launch_pdl(paged_merge_kernel<D, R, KTL, 1>, dim3(static_cast<unsigned>((units + 3) / 4), a.B), dim3(128), 0, st, p, rm);
+    return launch_pdl(paged_merge_kernel<D, R, KT, kWarps, 4>, dim3(static_cast<unsigned>(units), a.B, merge_depth(a, R)), dim3(128), 0, st, p, rm);
+  return launch_pdl(paged_merge_kernel<D, R, KT, kWarps, 1>, dim3(static_cast<unsigned>((units + 3) / 4), a.B, merge_depth(a, R)), dim3(128), 0, st, p, rm);
 }
 
 template <int D, int R>
@@ -1267,9 +1111,10 @@ cudaError_t launch_rows(const PagedArgs &a, const AttnParams &p, int ctas, cudaS
 }  // namespace
 
 long long paged_attention_units(const PagedArgs &a) {
-  const long long R = pick_rows(a), G = a.H / a.Hkv;
+  const bool tc = use_tc(a);
+  const long long R = tc ? paged_tc_rows() : pick_rows(a), G = a.H / a.Hkv;
   const long long cap = static_cast<long long>(a.max_pages) << a.page_log2;
-  const long long tiles = (cap >> key_tile_log2(a)) + 1;
+  const long long tiles = cap / (tc ? paged_tc_keys() : 1 << key_tile_log2(a)) + 1;
   const long long row_tiles = a.tokens * G / R + a.B;
   return row_tiles * tiles * a.Hkv;
 }
@@ -1303,9 +1148,11 @@ cudaError_t paged_attention(const PagedArgs &a, cudaStream_t st) {
   p.G = a.H / a.Hkv;
   p.by_g = fast_div(p.G);
   p.by_hkv = fast_div(a.Hkv);
-  p.by_warps = fast_div(static_cast<uint32_t>(ctas * kWarps));
-  p.warps = ctas * kWarps;
+  const bool tc = use_tc(a);
+  p.warps = tc ? ctas : ctas * kWarps;
+  p.by_warps = fast_div(static_cast<uint32_t>(p.warps));
   p.scale_log2 = static_cast<float>(a.scale * 1.4426950408889634);
+  if (tc) return paged_attention_tc(a, &p, ctas, st);
   switch (a.D) {
     case 16: return launch_rows<16>(a, p, ctas, st);
     case 32: return launch_rows<32>(a, p, ctas, st);

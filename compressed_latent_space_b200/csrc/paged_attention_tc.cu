@@ -1,0 +1,589 @@
+// Attention of many new tokens per sequence (pieces of a prompt) over a paged cache held in 4 bits,
+// on the 5th-generation tensor cores.  The same operator, rows and line of work units as
+// paged_attention.cu; a work item is 256 rows of one (sequence, head), a unit a tile of 96 keys.
+//
+// One CTA per SM walks a run of units.  It owns two query tiles of 128 rows that share every key
+// tile and take turns on the tensor cores:
+//   warps 0..7   softmax, one row a thread (warp w: tile w / 4, TMEM lanes 32 (w % 4)..), online
+//                with lazy rescaling; probabilities in float16 pairs over the tile's own scores in
+//                TMEM, where the P V product reads them as its A operand.  At the start of a run's
+//                item the same threads bring their query row into shared memory.
+//   warp 8       allocates TMEM and issues the products (one elected lane).
+//   warps 9..11  turn cached rows into operands: lane l of warp w unpacks key 32 (w - 9) + l of
+//                the tile, codes to float16 values n scale + zero in one rounding (a half-precision
+//                FMA), into the swizzled rows that the products read, a tile ahead in registers.
+// A code pair n_i, n_{i+4} leaves a word with one mask, so within eight channels the operands hold
+// them in the order 0 4 1 5 2 6 3 7: the queries are stored in that order too, and the output is
+// read back from it.
+//
+// Rounding: the held keys and values to float16 (2^-11 of each, which the single-token kernel does
+// not need, as it multiplies by bare codes: here that would cost two more operations per score,
+// and scores outnumber unpacked channels by four to one), queries in float16 times a power of two
+// per row (exact but for channels 2^28 below the row's largest), probabilities to float16; sums in
+// float32.  A key whose own or whose value's vector is not finite becomes NaN and its value zero,
+// so that the rows that see it, and no others, get NaN.
+//
+// What bounds it: the exponential and FMA pipes of the softmax, as in the dense attention (three
+// probability pairs in sixteen by a cubic on the FMA pipes); unpacking is a tenth of the instructions.
+// Every wait is bounded; on a timeout the CTA records it in the status word, stops, and releases
+// its tensor memory.
+#include "paged_attention.cuh"
+
+namespace cca {
+namespace {
+
+constexpr int TM = 128;          // rows of a query tile
+constexpr int TN = 96;           // keys of a tile
+constexpr int TC_ROWS = 2 * TM;  // rows of an item
+constexpr int TC_SOFT = 8, TC_MMA = 8, TC_UNPACK = 9, TC_UNPACKERS = 3;
+constexpr int TC_WARPS = TC_SOFT + 1 + TC_UNPACKERS;
+constexpr int TC_RING = 3;       // K and V tiles in shared memory
+constexpr float kTau = 8.0f;     // lazy-rescale threshold, log2 units
+static_assert(TC_UNPACKERS * 32 == TN, "an unpacking lane per key");
+static_assert(TC_WARPS == 12, "three warps per scheduler leave 168 registers a thread");
+
+template <int D>
+struct TcCfg {
+  static constexpr int NCH = D == 128 ? 2 : 1;         // 64-channel chunks per row
+  static constexpr int CW = D / NCH;
+  static constexpr int ROWB = CW * 2;                  // bytes of a chunk row (<= 128)
+  static constexpr int Q_CHUNK = TM * ROWB, Q_BYTES = NCH * Q_CHUNK;
+  static constexpr int KV_CHUNK = TN * ROWB, KV_BYTES = NCH * KV_CHUNK;
+  static constexpr uint32_t SW_MODE = ROWB == 128 ? 2u : 4u;
+  static constexpr int SBO = 8 * ROWB;
+  static constexpr int OFF_K = 2 * Q_BYTES;
+  static constexpr int OFF_V = OFF_K + TC_RING * KV_BYTES;
+  static constexpr int OFF_BAR = OFF_V + TC_RING * KV_BYTES;
+  static constexpr int OFF_PRE = OFF_BAR + 512;                // the units before each sequence
+  static constexpr uint32_t COL_O = 192;               // S_t at 96 t, O_t at 192 + D t
+  static_assert(COL_O + 2 * D <= 512, "S and O fit the TMEM allocation");
+  static_assert(ROWB == 128 || ROWB == 64, "two swizzles");
+  static_assert(Q_CHUNK % 1024 == 0 && KV_CHUNK % 1024 == 0, "swizzled chunks stay 1024-aligned");
+};
+
+// Byte of 16-byte piece `c` (of D / 8) of row `r` in a tile of `rows`-row chunks.
+template <int D>
+__device__ __forceinline__ uint32_t tc_piece(int r, int c, int chunk_bytes) {
+  using C = TcCfg<D>;
+  constexpr int PPC = C::ROWB / 16;
+  const int ch = c / PPC, cc = c % PPC;
+  const int sw = C::ROWB == 128 ? (r & 7) : ((r >> 1) & 3);
+  return static_cast<uint32_t>(ch * chunk_bytes + r * C::ROWB + ((cc ^ sw) << 4));
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ bool tc_elect() {
+  uint32_t pred;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(pred));
+  return pred != 0;
+}
+
+struct TcBars {
+  uint64_t q_full;
+  uint64_t k_full[TC_RING], k_empty[TC_RING], v_full[TC_RING], v_empty[TC_RING];
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint32_t tmem_base;
+  int abort;
+  int red[TC_WARPS];
+};
+static_assert(sizeof(TcBars) <= 512, "");
+
+// Eight codes to eight float16 values (pairs 0 4, 1 5, 2 6, 3 7) of scale and zero.
+__device__ __forceinline__ void unpack8(uint32_t w, __half2 sc, __half2 ze, uint32_t (&o)[4]) {
+  const __half2 m1024 = __float2half2_rn(-1024.f), s16 = __float2half2_rn(0.0625f), m64 = __float2half2_rn(-64.f);
+  const uint32_t y = w >> 8;
+  // 1024 + n and 1024 + 16 n, exactly
+  const uint32_t h[4] = {(w & 0x000f000fu) | 0x64006400u, (w & 0x00f000f0u) | 0x64006400u,
+                         (y & 0x000f000fu) | 0x64006400u, (y & 0x00f000f0u) | 0x64006400u};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __half2 n = *reinterpret_cast<const __half2 *>(&h[i]);
+    n = (i & 1) ? __hfma2(n, s16, m64) : __hadd2(n, m1024);
+    n = __hfma2(n, sc, ze);
+    o[i] = *reinterpret_cast<const uint32_t *>(&n);
+  }
+}
+
+template <int D, bool QBF16>
+__global__ void __launch_bounds__(32 * TC_WARPS, 1) paged_tc_kernel(const __grid_constant__ AttnParams p) {
+  using C = TcCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  TcBars &bars = *reinterpret_cast<TcBars *>(smem + C::OFF_BAR);
+  int *pre = reinterpret_cast<int *>(smem + C::OFF_PRE);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = p.batch.B;
+  if (smem_u32(smem) & 1023u) {                      // the swizzled tiles need it
+    if (tid == 0) report(p.status, DEV_LAYOUT);
+    return;
+  }
+  if (tid == 0) {
+    mbar_init(&bars.q_full, TC_SOFT);
+    for (int i = 0; i < TC_RING; ++i) {
+      mbar_init(&bars.k_full[i], TC_UNPACKERS);
+      mbar_init(&bars.k_empty[i], 1);
+      mbar_init(&bars.v_full[i], TC_UNPACKERS);
+      mbar_init(&bars.v_empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars.s_full[t], 1);
+      mbar_init(&bars.p_full[t], 4);
+      mbar_init(&bars.o_done[t], 1);
+    }
+    bars.abort = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (warp == TC_MMA) {
+    tmem_alloc(&bars.tmem_base, 512);
+    tmem_relinquish();
+  }
+  // units before each sequence: thread i sums a run of sequences, then a scan over the threads
+  {
+    const int per = (B + 32 * TC_WARPS - 1) / (32 * TC_WARPS);
+    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const PagedSeq s = paged_seq(p.batch, b, p.status);
+      const int rts = row_tiles(s, TC_ROWS, p.G);
+      int u = 0;
+      for (int rt = 0; rt < rts; ++rt) u += tiles_of<TN>(s, rt, TC_ROWS, p.by_g);
+      pre[b + 1] = u * p.Hkv;
+      sum += u * p.Hkv;
+    }
+    int inc = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += x;
+    }
+    if (lane == 31) bars.red[warp] = inc;
+    __syncthreads();
+    int run = inc - sum;
+    for (int w = 0; w < warp; ++w) run += bars.red[w];
+    if (tid == 0) pre[0] = 0;
+    for (int b = b0; b < b1; ++b) {
+      run += pre[b + 1];
+      pre[b + 1] = run;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+  volatile int *abort = &bars.abort;
+  const int total = pre[B], upw = div(total + p.warps - 1, p.by_warps);
+  if (blockIdx.x == 0) {
+    for (int b = tid; b <= B; b += 32 * TC_WARPS) p.plan[b] = pre[b];
+    if (tid == 0) {
+      p.plan[B + 1] = upw;
+      p.plan[B + 2] = 1;
+    }
+  }
+  int u = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(blockIdx.x) * upw));
+  const int uend = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(blockIdx.x + 1) * upw));
+  // phases run on over the items of the run: items, key tiles, tiles of each query tile
+  uint32_t seg = 0, kt0 = 0, st0[2] = {0u, 0u}, od0[2] = {0u, 0u};
+  bool ok = true;
+
+  while (u < uend && ok) {
+    // ---- the item of unit u, the same for every warp
+    int b = 0;
+    for (int first = 0, n = B; n > 0;) {             // the last b with pre[b] <= u
+      const int each = (n + 31) >> 5, i = first + lane * each;
+      const unsigned below = __ballot_sync(0xffffffffu, i < first + n && pre[min(i, B)] <= u);
+      first += (31 - __clz(below)) * each;
+      n = each == 1 ? 0 : min(each, B - first);
+      b = first;
+    }
+    const PagedSeq s = paged_seq(p.batch, b, nullptr);
+    const int per_head = div(pre[b + 1] - pre[b], p.by_hkv);
+    const int h = div(u - pre[b], per_head, rcp(per_head));
+    int t0 = u - pre[b] - h * per_head, rt = 0, T;
+    while (t0 >= (T = tiles_of<TN>(s, rt, TC_ROWS, p.by_g))) {
+      t0 -= T;
+      ++rt;
+    }
+    const int t1 = min(T, t0 + (uend - u));
+    u += t1 - t0;
+    const int rows = s.n * p.G, r0 = rt * TC_ROWS, nt = t1 - t0;
+    // key tiles of the run's item that query tile t has: through its last row
+    auto tiles = [&](int t) {
+      if (r0 + t * TM >= rows) return 0;
+      const int last = min(s.n - 1, div(r0 + t * TM + TM - 1, p.by_g));
+      const int keys = max(0, min(s.len, s.len - s.n + last + 1));
+      return max(0, min(t1, max(1, (keys + TN - 1) / TN)) - t0);
+    };
+    const int n0 = tiles(0), n1 = tiles(1);
+
+    if (warp >= TC_UNPACK) {
+      // -------------------------------------------------------------- cached rows to operands
+      constexpr int CP = D / 32;                     // 16-byte pieces of codes per row
+      const int kl = (warp - TC_UNPACK) * 32 + lane; // the lane's key of a tile
+      auto slot_of = [&](int j) {                    // its row in the pages, -1: none
+        const int key = (t0 + j) * TN + kl;
+        if (j >= nt || key >= s.len) return -1;
+        const int page = paged_page(p.table, p.max_pages, p.n_pages, b, key >> p.page_log2, p.status);
+        return page < 0 ? -1 : ((page * p.Hkv + h) << p.page_log2) + (key & ((1 << p.page_log2) - 1));
+      };
+      uint4 kc[CP], vc[CP];
+      uint2 sz;
+      auto fetch = [&](int slot) {
+        sz = make_uint2(0u, 0u);                     // no row: zeros
+#pragma unroll
+        for (int i = 0; i < CP; ++i) kc[i] = vc[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (slot >= 0) {
+          const uint4 *k = reinterpret_cast<const uint4 *>(p.k + static_cast<size_t>(slot) * (D / 2));
+          const uint4 *v = reinterpret_cast<const uint4 *>(p.v + static_cast<size_t>(slot) * (D / 2));
+#pragma unroll
+          for (int i = 0; i < CP; ++i) {
+            kc[i] = k[i];
+            vc[i] = v[i];
+          }
+          sz = p.scales[slot];
+        }
+      };
+      auto put = [&](uint32_t base, const uint4 (&c)[CP], __half2 sc, __half2 ze, bool cap) {
+#pragma unroll
+        for (int i = 0; i < CP; ++i) {
+          const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t o[4];
+            unpack8(w[e], sc, ze, o);
+            if (cap) {
+              const __half2 top = __float2half2_rn(kF16Max), low = __float2half2_rn(-kF16Max);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const __half2 r = __hmin2_nan(__hmax2_nan(*reinterpret_cast<__half2 *>(&o[x]), low), top);
+                o[x] = *reinterpret_cast<const uint32_t *>(&r);
+              }
+            }
+            sts128(base + tc_piece<D>(kl, 4 * i + e, C::KV_CHUNK), o[0], o[1], o[2], o[3]);
+          }
+        }
+      };
+      fetch(slot_of(0));
+      int next = slot_of(1);
+      for (int j = 0; j < nt && ok; ++j) {
+        const uint32_t g = kt0 + j;
+        const int st = g % TC_RING;
+        const uint32_t free_phase = ((g / TC_RING) & 1u) ^ 1u;
+        __half2 ks = __half2half2(__low2half(*reinterpret_cast<__half2 *>(&sz.x)));
+        __half2 kz = __half2half2(__high2half(*reinterpret_cast<__half2 *>(&sz.x)));
+        __half2 vs = __half2half2(__low2half(*reinterpret_cast<__half2 *>(&sz.y)));
+        __half2 vz = __half2half2(__high2half(*reinterpret_cast<__half2 *>(&sz.y)));
+        const float kt = fabsf(__low2float(kz)) + 15.f * fabsf(__low2float(ks));
+        const float vt = fabsf(__low2float(vz)) + 15.f * fabsf(__low2float(vs));
+        // not finite: the key becomes NaN, the value zero.  (fabsf(x) < inf is false for NaN)
+        if (!(kt < INFINITY) || !(vt < INFINITY)) {
+          kz = __half2half2(__ushort_as_half(0x7fff));
+          vs = vz = __float2half2_rn(0.f);
+        }
+        // values near float16's end may round up past it
+        const bool cap = __any_sync(0xffffffffu, kt > 65000.f || vt > 65000.f);
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars.k_empty[st], free_phase, abort, p.status));
+        if (!ok) break;
+        put(smem_u32(smem + C::OFF_K + st * C::KV_BYTES), kc, ks, kz, cap);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.k_full[st]);
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars.v_empty[st], free_phase, abort, p.status));
+        if (!ok) break;
+        put(smem_u32(smem + C::OFF_V + st * C::KV_BYTES), vc, vs, vz, cap);
+        fetch(next);
+        next = slot_of(j + 2);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.v_full[st]);
+      }
+    } else if (warp == TC_MMA) {
+      // -------------------------------------------------------------- products
+      const bool leader = tc_elect();
+      constexpr uint32_t idesc_qk = idesc_f16_f32(TM, TN, 0, 0, 1);
+      constexpr uint32_t idesc_pv = idesc_f16_f32(TM, D, 0, 1, 1);
+      constexpr int KSTEPS = D / 16, KPC = C::CW / 16;
+      auto issue_qk = [&](int t, int j) {            // S_t = Q_t K_j^T
+        const uint64_t qd = smem_desc(smem_u32(smem + t * C::Q_BYTES), 16, C::SBO, C::SW_MODE);
+        const uint64_t kd = smem_desc(smem_u32(smem + C::OFF_K + ((kt0 + j) % TC_RING) * C::KV_BYTES), 16,
+                                      C::SBO, C::SW_MODE);
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < KSTEPS; ++kk) {
+            const uint32_t qo = ((kk / KPC) * C::Q_CHUNK + (kk % KPC) * 32) >> 4;
+            const uint32_t ko = ((kk / KPC) * C::KV_CHUNK + (kk % KPC) * 32) >> 4;
+            umma_f16_ss(tmem + t * TN, qd + qo, kd + ko, idesc_qk, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&bars.s_full[t]);
+        }
+        __syncwarp();
+      };
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_full, seg & 1u, abort, p.status) &&
+                                       mbar_wait(&bars.k_full[kt0 % TC_RING], (kt0 / TC_RING) & 1u, abort, p.status));
+      if (ok) {
+        tc_fence_after();
+        if (n0 > 0) issue_qk(0, 0);
+        if (n1 > 0) issue_qk(1, 0);
+        if (leader) umma_commit(&bars.k_empty[kt0 % TC_RING]);
+        __syncwarp();
+      }
+      for (int j = 0; ok && j < nt; ++j) {
+        const uint32_t g = kt0 + j, g1 = g + 1;
+        const bool more = j + 1 < nt;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars.v_full[g % TC_RING], (g / TC_RING) & 1u, abort, p.status));
+        if (ok && more)
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars.k_full[g1 % TC_RING], (g1 / TC_RING) & 1u, abort, p.status));
+        if (!ok) break;
+        const uint64_t vd = smem_desc(smem_u32(smem + C::OFF_V + (g % TC_RING) * C::KV_BYTES), C::KV_CHUNK,
+                                      C::SBO, C::SW_MODE);
+        for (int t = 0; t < 2; ++t) {
+          const int n = t ? n1 : n0;
+          if (j >= n) continue;
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars.p_full[t], (st0[t] + j) & 1u, abort, p.status));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t tS = tmem + t * TN, tO = tmem + C::COL_O + t * D;
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < TN / 16; ++kk)     // 16 keys of P = 8 TMEM columns of pairs
+              umma_f16_ts(tO, tS + kk * 8, vd + kk * (2 * C::SBO / 16), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+            if (j + 1 >= n) umma_commit(&bars.o_done[t]);
+          }
+          __syncwarp();
+          if (j + 1 < n) issue_qk(t, j + 1);         // runs after this P V: it overwrites P_t
+        }
+        if (!ok) break;
+        if (leader) {
+          umma_commit(&bars.v_empty[g % TC_RING]);
+          if (more) umma_commit(&bars.k_empty[g1 % TC_RING]);
+        }
+        __syncwarp();
+      }
+    } else {
+      // -------------------------------------------------------------- softmax
+      const int t = warp >> 2, quad = warp & 3, lr = quad * 32 + lane;
+      const int n = t ? n1 : n0, r = r0 + t * TM + lr;
+      const bool live = r < rows;
+      const int tok = live ? div(r, p.by_g) : 0, hh = h * p.G + (live ? r - tok * p.G : 0);
+      // keys that the row sees (a row past the last one: as many as there are, its result unused)
+      const int lim = live ? min(s.len, s.len - s.n + tok + 1) : s.len;
+      const int lim_min = __reduce_min_sync(0xffffffffu, lim);
+      // the query row, times +-2^(14 - floor(log2 of its largest)), in the operands' order
+      float rs = 0.f;
+      {
+        uint4 w[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (live) {
+          const uint4 *src = reinterpret_cast<const uint4 *>(
+              static_cast<const uint16_t *>(p.q.ptr) + row_offset(p.q, p.batch.cu != nullptr, s, b, tok, hh));
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) w[i] = src[i];
+        }
+        auto val = [&](int c) {
+          const uint4 &q4 = w[c >> 3];
+          const int i = (c & 7) >> 1;
+          const uint32_t x = i == 0 ? q4.x : i == 1 ? q4.y : i == 2 ? q4.z : q4.w;
+          const uint32_t hx = (c & 1) ? x >> 16 : x & 0xffffu;
+          if constexpr (QBF16) return __uint_as_float(hx << 16);
+          else return __half2float(__ushort_as_half(static_cast<unsigned short>(hx)));
+        };
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < D; ++c) top = fmaxf(top, fabsf(val(c)));
+        int e = static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127;
+        e = max(-100, min(100, e));
+        float f = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+        rs = fabsf(p.scale_log2) * __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+        if (p.scale_log2 < 0.f) f = -f;              // rs stays positive: the maximum is taken of raw scores
+        const uint32_t base = smem_u32(smem + t * C::Q_BYTES);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          sts128(base + tc_piece<D>(lr, i, C::Q_CHUNK), pack_f16x2(val(8 * i) * f, val(8 * i + 4) * f),
+                 pack_f16x2(val(8 * i + 1) * f, val(8 * i + 5) * f),
+                 pack_f16x2(val(8 * i + 2) * f, val(8 * i + 6) * f),
+                 pack_f16x2(val(8 * i + 3) * f, val(8 * i + 7) * f));
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.q_full);
+      }
+      const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+      const uint32_t tS = tmem + t * TN + lane_off, tO = tmem + C::COL_O + t * D + lane_off;
+      const uint64_t sc2 = f2(rs, rs);
+      float m_ref = -INFINITY, l = 0.f;
+      bool poison = false;                           // a score that is NaN or +inf
+      for (int j = 0; ok && j < n; ++j) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars.s_full[t], (st0[t] + j) & 1u, abort, p.status));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t x[TN];
+#pragma unroll
+        for (int c = 0; c < TN / 32; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[c * 32]));
+        tmem_ld_wait();
+        if ((t0 + j + 1) * TN > lim_min) {           // some row of the warp does not see all of it
+          const int seen = lim - (t0 + j) * TN;
+#pragma unroll
+          for (int i = 0; i < TN; ++i)
+            if (i >= seen) x[i] = __float_as_uint(-INFINITY);
+        }
+        float mx4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          mx4[e] = max3_nan(-INFINITY, __uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+#pragma unroll
+        for (int i = 8; i < TN; i += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx4[e] = max3_nan(mx4[e], __uint_as_float(x[i + 2 * e]), __uint_as_float(x[i + 2 * e + 1]));
+        const float mx = max3_nan(max3_nan(mx4[0], mx4[1], mx4[2]), mx4[3], -INFINITY) * rs;
+        poison = poison || !(mx < INFINITY);
+        const bool resc = mx > m_ref + kTau;
+        const float scale = resc ? ex2(m_ref - mx) : 1.f;   // (0 for the first visible key)
+        if (resc) m_ref = mx;
+        l *= scale;
+        if (j > 0 && __any_sync(0xffffffffu, resc)) {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(tO + c * 16, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
+            tmem_st16(tO + c * 16, o);
+          }
+        }
+        // (a row that has seen no key yet: every score is -inf, any finite reference does)
+        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+        const uint64_t nm2 = f2(-mu, -mu);
+        uint64_t l2[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < TN / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int i = c * 32 + 2 * e;
+            const uint64_t x2 = fma2(f2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sc2, nm2);
+            float p0, p1;
+            if (D < 128 && e % 5 == 4) {             // pairs 4, 9, 14 of 16: FMA pipes
+              ex2_poly2(x2, p0, p1);
+            } else {
+              float y0, y1;
+              unf2(x2, y0, y1);
+              p0 = ex2(y0);
+              p1 = ex2(y1);
+            }
+            l2[e & 3] = add2(l2[e & 3], f2(p0, p1));
+            pk[e] = pack_f16x2(p0, p1);
+          }
+          tmem_st16(tS + c * 16, pk);
+        }
+        float a0, a1;
+        unf2(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])), a0, a1);
+        l += a0 + a1;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[t]);
+      }
+      if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars.o_done[t], od0[t] & 1u, abort, p.status));
+      if (ok) {
+        tc_fence_after();
+        // a row without a visible key summed the cubic's 2^-125s, or nothing
+        if (m_ref == -INFINITY) l = 0.f;
+        if (poison) l = __uint_as_float(0x7fc00000u);
+        const bool whole = t0 == 0 && t1 == T;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const size_t off = live ? out_offset(p, s, b, h, r) : 0;
+        const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0)) * TC_ROWS + t * TM + lr;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint32_t o[8];
+          __syncwarp();
+          if (n > 0) {
+            tmem_ld8(tO + c * 8, o);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = 0u;
+          }
+          // back from the operands' order 0 4 1 5 2 6 3 7
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = l == 0.f ? 0.f : __uint_as_float(o[2 * e]);
+            v[4 + e] = l == 0.f ? 0.f : __uint_as_float(o[2 * e + 1]);
+          }
+          if (live && whole) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= inv;
+            store_row<8>(p.o, p.o_lo, off + c * 8, v);
+          } else if (live) {
+            float4 *d = reinterpret_cast<float4 *>(p.part_o + at * D + c * 8);
+            d[0] = make_float4(v[0], v[1], v[2], v[3]);
+            d[1] = make_float4(v[4], v[5], v[6], v[7]);
+          }
+        }
+        if (live && !whole) p.part_ml[at] = make_float2(m_ref, l);
+      }
+      tc_fence_before();
+    }
+    ok = __syncthreads_and(ok);                      // Q, S, O are free for the next item
+    tc_fence_after();
+    ++seg;
+    kt0 += nt;
+    st0[0] += n0;
+    st0[1] += n1;
+    od0[0] += n0 > 0;
+    od0[1] += n1 > 0;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == TC_MMA) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool QBF16>
+cudaError_t launch(const PagedArgs &a, const AttnParams &p, int ctas, cudaStream_t st) {
+  const size_t smem = TcCfg<D>::OFF_PRE + (static_cast<size_t>(a.B) + 1) * 4;
+  cudaError_t e = ensure_dyn_smem<paged_tc_kernel<D, QBF16>>(smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_tc_kernel<D, QBF16>, dim3(ctas), dim3(32 * TC_WARPS), smem, st, p);
+  if (e != cudaSuccess) return e;
+  const long long rows = static_cast<long long>(a.cu ? a.tokens : a.tokens / a.B) * p.G;
+  const int rm = static_cast<int>(rows < TC_ROWS ? rows : TC_ROWS);
+  const unsigned gx = static_cast<unsigned>((static_cast<long long>(rm) * a.Hkv + 3) / 4);
+  return launch_pdl(paged_merge_kernel<D, TC_ROWS, TN, 1, 1>, dim3(gx, a.B, merge_depth(a, TC_ROWS)), dim3(128), 0, st, p, rm);
+}
+
+}  // namespace
+
+int paged_tc_rows() { return TC_ROWS; }
+int paged_tc_keys() { return TN; }
+
+cudaError_t paged_attention_tc(const PagedArgs &a, const void *params, int ctas, cudaStream_t st) {
+  const AttnParams &p = *static_cast<const AttnParams *>(params);
+  const bool bf = a.q.dtype == CCA_BF16;
+  switch (a.D) {
+    case 32: return bf ? launch<32, true>(a, p, ctas, st) : launch<32, false>(a, p, ctas, st);
+    case 64: return bf ? launch<64, true>(a, p, ctas, st) : launch<64, false>(a, p, ctas, st);
+    case 128: return bf ? launch<128, true>(a, p, ctas, st) : launch<128, false>(a, p, ctas, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace cca

@@ -55,17 +55,17 @@ def attention(q, k, v, scale, vz=None):
     n, H, d = q.shape
     L, Hkv, _ = k.shape
     o, mass, mag = np.zeros((n, H, d)), np.zeros((n, H, d)), np.zeros((n, H))
-    for i in range(n):
-        end = L - n + i + 1
-        if end <= 0:
-            continue
-        for h in range(H):
-            g = h // (H // Hkv)
-            s = k[:end, g] @ q[i, h] * scale
-            p = np.exp(s - s.max())
-            p /= p.sum()
-            o[i, h] = p @ v[:end, g]
-            a = np.abs(v[:end, g]) if vz is None else np.abs(v[:end, g]) + np.abs(vz[:end, g])[:, None]
-            mass[i, h] = p @ a
-            mag[i, h] = (np.abs(k[:end, g]) @ np.abs(q[i, h])).max() * scale
+    if L == 0:
+        return o, mass, mag
+    seen = np.arange(L)[None] < (L - n + np.arange(n) + 1)[:, None]          # [n, L]
+    some = seen.any(1)
+    for h in range(H):
+        g = h // (H // Hkv)
+        s = np.where(seen, q[:, h] @ k[:, g].T * scale, -np.inf)
+        p = np.exp(s - np.where(some, s.max(1, initial=-np.inf), 0.0)[:, None])
+        p /= np.where(some, p.sum(1), 1.0)[:, None]
+        o[:, h] = p @ v[:, g]
+        a = np.abs(v[:, g]) if vz is None else np.abs(v[:, g]) + np.abs(vz[:, g])[:, None]
+        mass[:, h] = p @ a
+        mag[:, h] = np.where(seen, np.abs(q[:, h]) @ np.abs(k[:, g]).T, 0.0).max(1) * abs(scale)
     return o, mass, mag

@@ -76,7 +76,7 @@ class Batch:
         x = self.rng.standard_normal((self.tokens, heads, self.d)) * std
         return torch.as_tensor(x).to(dtype or self.dtype)
 
-    def attention(self, q, scale=None):
+    def attention(self, q, scale=None, tensor=False):
         """(o, tolerance) [tokens, H, d] in float64.
 
         The tolerance, in the kernel's order of rounding:
@@ -88,17 +88,23 @@ class Batch:
           a score sums products in float32 (a relative 2^-20 of the magnitudes' sum covers d <=
           128 terms and the scale's and exponential's own roundings), which moves every weight
           by as much;
+          with `tensor` (4 bits, many rows a sequence) held keys and values are rounded to float16
+          (2^-11 of the magnitudes behind a score, and of the values), and some exponentials come
+          from a cubic (2^-13);
           the result is rounded to its type (half a step)."""
         outs, tols, t0 = [], [], 0
         sc = self.d ** -0.5 if scale is None else scale
         w = 2.0 ** -16 if self.bits == 16 and self.dtype == torch.bfloat16 else 2.0 ** -11
+        s = 2.0 ** -20
+        if tensor:
+            w, s = 2.0 ** -10 + 2.0 ** -13, s + 2.0 ** -11
         for b, n in enumerate(self.new):
             k, v = self.held[b]
             qb = q[t0:t0 + n].double().numpy()
             o, mass, mag = P.attention(qb, k, v, sc, self.vz[b])
             top = np.abs(v).max() if v.size else 0.0
             small = len(v) * 2.0 ** -25 * 2 * top
-            tols.append(mass * (w + 2.0 ** -20 * (1 + mag[..., None])) + small
+            tols.append(mass * (w + 2.0 ** -20 + s * mag[..., None]) + small
                         + np.abs(o) * HALF_STEP[q.dtype] + 1e-7)
             outs.append(o)
             t0 += n

@@ -346,6 +346,69 @@ def test_attention_nonfinite_rows_stay_with_those_who_see_them(cuda_lib, bits):
         assert torch.isnan(o[6:]).any(-1).all()
 
 
+# many rows a sequence: the tensor-core kernel (4 bits, d~ >= 32)
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d,page,G", [(32, 16, 4), (64, 64, 4), (64, 16, 3), (128, 32, 8), (64, 32, 1)])
+@pytest.mark.parametrize("new,past", [((70, 300, 0, 1, 129), (0, 500, 9, 700, 33)), ((640, 3, 257), (1000, 0, 2))])
+def test_attention_prompt_pieces(cuda_lib, dtype, d, page, G, new, past):
+    """Ragged pieces beside single tokens and empty slots: row tiles and key tiles that end inside
+    each other, runs that hold the end of one item and the start of the next."""
+    cls = cuda_lib
+    Hkv = 2
+    if G == 1:
+        new = tuple(2 * n for n in new)
+    t = Batch([n + p for n, p in zip(new, past)], list(new), Hkv, d, page, 4, dtype, seed=d + G)
+    q = t.rows(Hkv * G)
+    cache = t.cache(cls)
+    o = cache.attend(q.cuda(), cu_seqlens=t.cu.cuda())
+    ref, tol = t.attention(q, tensor=True)
+    assert_within(o, ref, tol, f"{dtype} d={d} G={G}")
+    cache.check()
+    again = cache.attend(q.cuda(), cu_seqlens=t.cu.cuda())
+    assert torch.equal(o, again)
+
+
+def test_attention_prompt_piece_long_and_split(cuda_lib):
+    """One sequence: every CTA works on a piece of it; an explicit scale, of either sign; float32 out."""
+    cls = cuda_lib
+    t = Batch([6000], [130], 1, 64, 64, 4, torch.float16, seed=3, k_std=2.0)
+    q = t.rows(4)
+    for scale in (None, 0.3, -0.05):
+        o = t.cache(cls).attend(q.cuda(), scale=scale, out=torch.empty(130, 4, 64, device="cuda"))
+        ref, tol = t.attention(q, scale, tensor=True)
+        assert_within(o, ref, tol, f"scale {scale}")
+
+
+def test_attention_prompt_piece_positions_below_zero_and_extremes(cuda_lib):
+    """Lengths below the new tokens; values at float16's end; tiny and huge bfloat16 queries."""
+    cls = cuda_lib
+    t = Batch([100, 0, 300], [200, 200, 200], 1, 64, 16, 4, torch.bfloat16, seed=5, v_std=15000.0)
+    assert all(np.isfinite(v).all() for _, v in t.held)
+    q = t.rows(2)
+    q[:200] *= 1e-6
+    q[400:] *= 1e5
+    o = t.cache(cls).attend(q.cuda(), scale=1e-5, out=torch.empty(600, 2, 64, device="cuda"))
+    t.held[1] = (np.zeros((0, 1, 64)),) * 2
+    ref, tol = t.attention(q, 1e-5, tensor=True)
+    assert (o[:100] == 0).all() and (o[200:400] == 0).all()
+    assert_within(o, ref, tol + np.abs(ref) * 2.0 ** -24, "extremes")
+
+
+@pytest.mark.parametrize("which", [0, 1, 2, 3])
+def test_attention_prompt_piece_nonfinite_row(cuda_lib, which):
+    """A NaN in a cached vector's scale or zero reaches the rows that see it and no others."""
+    cls = cuda_lib
+    t = Batch([300, 300], [200, 200], 1, 64, 16, 4, torch.float16, seed=7)
+    cache = t.cache(cls)
+    q = t.rows(2)
+    clean = cache.attend(q.cuda()).clone()
+    pos = 250                                              # new token 150 of the second sequence
+    cache.scales[int(t.table[1, pos // 16]), 0, pos % 16, which] = float("nan")
+    o = cache.attend(q.cuda())
+    assert torch.equal(o[:350], clean[:350])
+    assert torch.isnan(o[350:]).all()
+
+
 # ------------------------------------------------------------------------------- kernel-side errors
 def test_bad_pages_are_reported_and_read_as_zeros(cuda_lib):
     cls = cuda_lib
