@@ -681,8 +681,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
   __shared__ int red[2][kWarps];
   __shared__ PieceAt at_piece[kWarps][2];            // what each warp leaves in shared memory
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();                           // (after the wait: the merge relies on it)
   if (lane < 2) at_piece[warp][lane].state = kNone;
   const int B = p.batch.B;
   int pad, upw;

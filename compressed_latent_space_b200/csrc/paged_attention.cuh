@@ -102,74 +102,86 @@ __device__ __forceinline__ void join(float &m, float &l, float4 &acc, float m2, 
   acc.w = acc.w * fa + v.w * fb;
 }
 
+// Rows that a warp of the merge takes: several where a tile has very many.
+constexpr int merge_rows(int R) { return R >= 128 ? 8 : 1; }
+
 // Joins the pieces of the items that more than one CTA (of RUNS runs) worked on: WPR warps per (row of a tile,
 // head, sequence).  D / 4 lanes hold the row's channels; the lane groups take pieces in turn and
 // are added in a fixed order.
 template <int D, int R, int KT, int RUNS, int WPR>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ AttnParams p, int rows_max) {
   constexpr int LN = D / 4, GW = 32 / LN, GR = GW * WPR, UN = 4;   // UN pieces in flight per group
+  constexpr int RPW = WPR == 1 ? merge_rows(R) : 1;  // rows of a warp
   __shared__ float so[WPR == 4 ? 4 : 1][D];
   __shared__ float2 sml[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit = WPR == 4 ? blockIdx.x : blockIdx.x * 4 + warp;
-  const int h = unit / rows_max, rr = unit - h * rows_max, b = blockIdx.y;
+  const int unit = WPR == 4 ? blockIdx.x : blockIdx.x * 4 + warp, per = (rows_max + RPW - 1) / RPW;
+  const int h = unit / per, rr0 = (unit - h * per) * RPW, b = blockIdx.y;
   const int ln = lane % LN, grp = (WPR == 4 ? warp * GW : 0) + lane / LN;
-  pdl_launch_dependents();
-  pdl_wait();
-  if (h >= p.Hkv) return;
+  // (the attention kernel lets this one start once its own predecessors are done, so lengths and
+  // cu_seqlens are final; what the attention writes is read behind the wait)
   const PagedSeq s = paged_seq(p.batch, b, nullptr);
-  const int p0 = p.plan[b], p1 = p.plan[b + 1], upw = p.plan[p.batch.B + 1], pad = p.plan[p.batch.B + 2];
   const int rows = s.n * p.G, rts = row_tiles(s, R, p.G);
-  if (rr >= rows) return;
-  const float rpad = rcp(pad);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (h >= p.Hkv || rr0 >= rows) return;
+  const int p0 = p.plan[b], p1 = p.plan[b + 1], upw = p.plan[p.batch.B + 1], pad = p.plan[p.batch.B + 2];
+  const float rpad = rcp(pad), rrun = rcp(upw * RUNS);
   int u0 = p0 + h * div(p1 - p0, p.by_hkv);
   for (int rt = 0; rt < rts; ++rt) {
-    const int T = tiles_of<KT>(s, rt, R, p.by_g);
-    const int ca = u0 / upw / RUNS, cz = (u0 + T - 1) / upw / RUNS, r = rt * R + rr;
+    const int T = tiles_of<KT>(s, rt, R, p.by_g), first = u0;
     u0 += padded(T, pad, rpad);
-    if (ca == cz || r >= rows || rt % gridDim.z != blockIdx.z) continue;
-    float m = 0.f, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c0 = ca + grp; c0 <= cz; c0 += UN * GR) {
-      float2 ml[UN];
-      float4 v[UN];
+    if (rt % gridDim.z != blockIdx.z) continue;
+    // the CTAs with its first and last tile
+    const int ca = div(first, upw * RUNS, rrun), cz = div(first + T - 1, upw * RUNS, rrun);
+    if (ca == cz) continue;
+#pragma unroll 1
+    for (int q = 0; q < RPW; ++q) {
+      const int rr = rr0 + q, r = rt * R + rr;
+      if (rr >= R || r >= rows) break;
+      float m = 0.f, l = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c0 = ca + grp; c0 <= cz; c0 += UN * GR) {
+        float2 ml[UN];
+        float4 v[UN];
 #pragma unroll
-      for (int i = 0; i < UN; ++i) {
-        const int c = c0 + i * GR;
-        const size_t at = (static_cast<size_t>(min(c, cz)) * 2 + (c == ca ? 1 : 0)) * R + rr;
-        ml[i] = c <= cz ? p.part_ml[at] : make_float2(0.f, 0.f);
-        v[i] = c <= cz ? *reinterpret_cast<const float4 *>(p.part_o + at * D + ln * 4)
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < UN; ++i) {
+          const int c = c0 + i * GR;
+          const size_t at = (static_cast<size_t>(min(c, cz)) * 2 + (c == ca ? 1 : 0)) * R + rr;
+          ml[i] = c <= cz ? p.part_ml[at] : make_float2(0.f, 0.f);
+          v[i] = c <= cz ? *reinterpret_cast<const float4 *>(p.part_o + at * D + ln * 4)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < UN; ++i) join(m, l, acc, ml[i].x, ml[i].y, v[i]);
       }
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < UN; ++i) join(m, l, acc, ml[i].x, ml[i].y, v[i]);
-    }
-    __syncwarp();
+      for (int off = LN; off < 32; off <<= 1) {      // the warp's groups, lower first
+        const float m2 = __shfl_down_sync(0xffffffffu, m, off), l2 = __shfl_down_sync(0xffffffffu, l, off);
+        float4 v;
+        v.x = __shfl_down_sync(0xffffffffu, acc.x, off);
+        v.y = __shfl_down_sync(0xffffffffu, acc.y, off);
+        v.z = __shfl_down_sync(0xffffffffu, acc.z, off);
+        v.w = __shfl_down_sync(0xffffffffu, acc.w, off);
+        join(m, l, acc, m2, l2, v);
+      }
+      if constexpr (WPR == 4) {
+        __syncthreads();
+        if (lane < LN) *reinterpret_cast<float4 *>(&so[warp][ln * 4]) = acc;
+        if (lane == 0) sml[warp] = make_float2(m, l);
+        __syncthreads();
+        if (warp == 0 && lane < LN)
 #pragma unroll
-    for (int off = LN; off < 32; off <<= 1) {        // the warp's groups, lower first
-      const float m2 = __shfl_down_sync(0xffffffffu, m, off), l2 = __shfl_down_sync(0xffffffffu, l, off);
-      float4 v;
-      v.x = __shfl_down_sync(0xffffffffu, acc.x, off);
-      v.y = __shfl_down_sync(0xffffffffu, acc.y, off);
-      v.z = __shfl_down_sync(0xffffffffu, acc.z, off);
-      v.w = __shfl_down_sync(0xffffffffu, acc.w, off);
-      join(m, l, acc, m2, l2, v);
-    }
-    if constexpr (WPR == 4) {
-      __syncthreads();
-      if (lane < LN) *reinterpret_cast<float4 *>(&so[warp][ln * 4]) = acc;
-      if (lane == 0) sml[warp] = make_float2(m, l);
-      __syncthreads();
-      if (warp == 0 && lane < LN)
-#pragma unroll
-        for (int i = 1; i < 4; ++i)
-          join(m, l, acc, sml[i].x, sml[i].y, *reinterpret_cast<const float4 *>(&so[i][ln * 4]));
-    }
-    if ((WPR == 1 || warp == 0) && lane < LN) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const float v[4] = {l == 0.f ? 0.f : acc.x * inv, l == 0.f ? 0.f : acc.y * inv,
-                          l == 0.f ? 0.f : acc.z * inv, l == 0.f ? 0.f : acc.w * inv};
-      store_row<4>(p.o, p.o_lo, out_offset(p, s, b, h, r) + ln * 4, v);
+          for (int i = 1; i < 4; ++i)
+            join(m, l, acc, sml[i].x, sml[i].y, *reinterpret_cast<const float4 *>(&so[i][ln * 4]));
+      }
+      if ((WPR == 1 || warp == 0) && lane < LN) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float v[4] = {l == 0.f ? 0.f : acc.x * inv, l == 0.f ? 0.f : acc.y * inv,
+                            l == 0.f ? 0.f : acc.z * inv, l == 0.f ? 0.f : acc.w * inv};
+        store_row<4>(p.o, p.o_lo, out_offset(p, s, b, h, r) + ln * 4, v);
+      }
     }
   }
 }

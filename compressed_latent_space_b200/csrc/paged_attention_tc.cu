@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(32 * TC_WARPS, 1) paged_tc_kernel(const __grid
     fence_mbar_init();
   }
   pdl_wait();
-  pdl_launch_dependents();
+  pdl_launch_dependents();                           // (after the wait: the merge relies on it)
   if (warp == TC_MMA) {
     tmem_alloc(&bars.tmem_base, 512);
     tmem_relinquish();
@@ -566,7 +566,7 @@ cudaError_t launch(const PagedArgs &a, const AttnParams &p, int ctas, cudaStream
   if (e != cudaSuccess) return e;
   const long long rows = static_cast<long long>(a.cu ? a.tokens : a.tokens / a.B) * p.G;
   const int rm = static_cast<int>(rows < TC_ROWS ? rows : TC_ROWS);
-  const unsigned gx = static_cast<unsigned>((static_cast<long long>(rm) * a.Hkv + 3) / 4);
+  const unsigned gx = static_cast<unsigned>((static_cast<long long>((rm + merge_rows(TC_ROWS) - 1) / merge_rows(TC_ROWS)) * a.Hkv + 3) / 4);
   return launch_pdl(paged_merge_kernel<D, TC_ROWS, TN, 1, 1>, dim3(gx, a.B, merge_depth(a, TC_ROWS)), dim3(128), 0, st, p, rm);
 }
 
