@@ -681,6 +681,8 @@ int check_paged_step(const cca_config_t *cfg, const cca_paged_cache_t *cache, cc
   if (rc) return rc;
   if ((rc = check_decode_shape(d))) return rc;
   if (!d.bf16) return fail(CCA_ERR_UNSUPPORTED, "the paged decode step runs bfloat16 layers");
+  if (d.G > 8)
+    return fail(CCA_ERR_UNSUPPORTED, "decode takes at most 8 query heads per kv head (got %d)", d.G);
   if ((rc = cca::check_paged_cache(cache, pa))) return rc;
   if (pa.Hkv != d.Hkv || pa.D != d.DL)
     return fail(CCA_ERR_INVALID_ARG, "pages of %d heads of %d, the layer has %d of %d", pa.Hkv, pa.D, d.Hkv, d.DL);

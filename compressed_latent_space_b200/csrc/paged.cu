@@ -69,6 +69,14 @@ struct Raw8 {
   }
 };
 
+// rope_cos_sin_turns with the library's accurate sine and cosine of half turns: a 4-bit key that
+// falls on the other side of a rounding is off by a whole step, and the hardware approximation's
+// 1e-6 made that twice as frequent as float32 itself does.
+__device__ __forceinline__ void rope_turns_exact(int t, float hi, float lo, float &c, float &s) {
+  const float tf = static_cast<float>(t), prod = tf * hi, err = fmaf(tf, hi, -prod);
+  sincospif(2.f * ((prod - rintf(prod)) + fmaf(tf, lo, err)), &s, &c);
+}
+
 // The codes of eight elements at zero z and scale sc > 0, element e in bits 4 e ..: the quotient
 // by a reciprocal, good to 15 2^-22, and where that leaves a rounding open (within 1e-5 of a half)
 // by the division itself.
@@ -170,7 +178,7 @@ __global__ void __launch_bounds__(256, 4) paged_append_kernel(const __grid_const
   float cs[8], sn[8];
   if (p.rotate && row < kv0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) rope_cos_sin_turns(pos, thi[c0 + j], tlo[c0 + j], cs[j], sn[j]);
+    for (int j = 0; j < 8; ++j) rope_turns_exact(pos, thi[c0 + j], tlo[c0 + j], cs[j], sn[j]);
   }
   // (rpt is the same for all lanes: they leave the loop together)
 #pragma unroll 1

@@ -7,8 +7,13 @@
 //
 // Mathematics, 4 bits (k_j = ks_j n_j + kz_j, v_j = vs_j u_j + vz_j with codes n, u in 0..15):
 //   s_j = c (q . k_j) = (c ks_j) (q . n_j) + kz_j (c sum q)
-//   o   = sum_j p_j v_j = sum_j (p_j vs_j) u_j + sum_j p_j vz_j
-// so the tensor cores multiply by the bare codes and the scales are applied to one score per
+//   o   = sum_j p_j v_j = sum_j w_j u_j + sum_j p_j vz_j,   w_j = p_j vs_j
+// The tensor cores take w_j rounded to float16, w~_j, whose errors the codes u (0 to 15, never
+// centred) would weigh 2.6 times as heavily as the values; so the middle of the codes is taken out
+// of the rounded part again (one more row of the product, of ones, sums w~):
+//   o   = sum_j w~_j u_j - 7.5 sum_j w~_j + sum_j p_j (vz_j + 7.5 vs_j)
+// (error against 64 bits at 8k keys 5.1e-4 without, 3.0e-4 with it, 2.1e-4 of that the result's
+// own rounding, for 3 % of the time).  So the tensor cores multiply by the bare codes and the scales are applied to one score per
 // (key, row) instead of d~ channels.  A code needs no conversion either: n in the low bits of a
 // float16 is the subnormal n 2^-24, and four bits further up n 2^-20, so `word & 0x000f000f` and
 // `word & 0x00f000f0` are pairs of operands, exact, and the powers of two go into the queries
@@ -167,6 +172,7 @@ struct Core {
   float ksf;                     // factor of a raw score into log2 units
   float m[NT][2], l[NT][2], z[NT][2];
   float o[MT][NT][4];
+  float ws[NT][4];               // sums of the rounded weights (4 bits): [nt][col]
   float vlim;                    // 2^(7 - e)
   float vexp;                    // e of the value scales (4 bits)
   bool first;                    // no tile yet: m is not a maximum
@@ -284,6 +290,8 @@ struct Core {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) m[nt][e] = l[nt][e] = z[nt][e] = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) ws[nt][0] = ws[nt][1] = ws[nt][2] = ws[nt][3] = 0.f;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -501,7 +509,7 @@ struct Core {
           uint64_t acc = add2(f2(l[nt][0], l[nt][1]), p2);
           unf2(acc, l[nt][0], l[nt][1]);
           if constexpr (BITS == 4) {
-            const float vs = vzs[f][half].x, vz = vzs[f][half].y;
+            const float vs = vzs[f][half].x, vz = fmaf(7.5f, vs, vzs[f][half].y);
             float w0, w1, z0, z1;
             unf2(mul2(p2, f2(vs, vs)), w0, w1);
             unf2(fma2(p2, f2(vz, vz), f2(z[nt][0], z[nt][1])), z0, z1);
@@ -532,6 +540,12 @@ struct Core {
       for (int nt = 0; nt < NT; ++nt) {
         px[nt][0] = X == 1 || g / GP == x ? pb[f][nt][0] : 0u;
         px[nt][1] = X == 1 || g / GP == x ? pb[f][nt][1] : 0u;
+      }
+      if constexpr (BITS == 4) {
+        constexpr uint32_t one2 = 0x3c003c00u;
+        const uint32_t ones[4] = {one2, one2, one2, one2};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(ws[nt], ones, px[nt]);
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -601,6 +615,7 @@ struct Core {
         m[nt][col] = now;
         l[nt][col] *= al;
         z[nt][col] *= al;
+        ws[nt][col] *= al;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           o[mt][nt][col] *= al;
@@ -635,7 +650,8 @@ struct Core {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[mt][nt][e] = fmaf(o[mt][nt][e], e < 2 ? f0 : f1, z[nt][e & 1]);
+          for (int e = 0; e < 4; ++e)
+            o[mt][nt][e] = fmaf(o[mt][nt][e], e < 2 ? f0 : f1, fmaf(-7.5f, ws[nt][e & 1], z[nt][e & 1]));
     }
     if constexpr (X > 1) {
 #pragma unroll

@@ -114,6 +114,8 @@ class CCALayer:
     def _prefill_paged(self, x, cache: PagedCache, out, stream):
         # the forward over dense keys and values, which go on into the pages rotated already
         B, S, _ = x.shape
+        if cache.vshift_state is None or cache.status is None:
+            raise ValueError("a layer's paged cache comes from new_paged_cache")
         if B != cache.batch or S > cache.max_pages * cache.page_size:
             raise ValueError(f"{B} x {S} tokens do not fit a paged cache of {cache.batch} x "
                              f"{cache.max_pages * cache.page_size}")

@@ -151,6 +151,8 @@ class PagedCache:
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.gather(tokens, cu_seqlens, k_out, v_out, dtype)
+        if (k_out is None) != (v_out is None) or (k_out is None and tokens is None):
+            raise ValueError("gather takes k_out and v_out, or the number of tokens")
         if k_out is None:
             dt = dtype or (torch.float16 if self.scales is not None else self.k.dtype)
             k_out, v_out = torch.empty((2, tokens, self.n_kv_heads, self.head_dim), dtype=dt,

@@ -275,8 +275,8 @@ CCA_API int cca_cache_check(cca_cache_t *cache, void *stream);
  *               holds no sequence: nothing is stored for it and its output rows are zero
  *   status      int32 sticky error word, or NULL; read and cleared by cca_paged_check
  * head_dim in {16, 32, 64, 128}; page_size a power of two in [16, 4096]; max_pages * page_size
- * <= 2^24; batch <= 4096; n_pages * n_kv_heads * page_size < 2^31.  Two sequences may share
- * pages they only read; rows behind a sequence's length are never read as data and may hold
+ * <= 2^24; batch and n_kv_heads <= 4096; n_pages * n_kv_heads * page_size < 2^31; at most 2^24
+ * (token, head) rows a call.  Two sequences may share pages they only read; rows behind a sequence's length are never read as data and may hold
  * anything.
  *
  * 4 bits: a vector x (keys after the rotation) is held as zero = f16(min x), scale =
@@ -307,7 +307,8 @@ typedef struct {
 } cca_paged_cache_t;
 
 /* Rows of a [token, head, channel] tensor of CCA_F32, CCA_BF16 or CCA_F16; channels contiguous,
- * strides in elements, ptr and strides multiples of 16 bytes.  New tokens come
+ * strides in elements, ptr and strides multiples of 16 bytes, token_stride and head_stride below
+ * 2^31.  New tokens come
  *   packed   (cu_seqlens given, [batch + 1] int32 on the device): token i of sequence b, head h
  *            at ptr + (cu_seqlens[b] + i) * token_stride + h * head_stride.  Rows from
  *            cu_seqlens[batch] on are neither read nor written.
@@ -356,8 +357,12 @@ CCA_API size_t cca_paged_attention_workspace_size(const cca_paged_cache_t *cache
  *   o = softmax(scale q k^T) v       (scale 0: 1 / sqrt(head_dim))
  * q is CCA_F16 or CCA_BF16 (at 16 bits the pages' type), o any type.  A query that sees no key
  * (length 0, or a position below 0) gets a row of zeros.  An infinity or NaN in a cached row
- * reaches the rows that see it, and at 16 bits may reach the other new tokens of that sequence
- * in the same call.
+ * reaches the rows that see it; at 16 bits a value's may also reach the new tokens before it
+ * of the same sequence and call.
+ * Rounding: probabilities (times the value's scale, at 4 bits) to float16 (two bfloat16 terms
+ * over bfloat16 pages), the result to o's type; everything else in float32.  Where a sequence
+ * has 112 rows (tokens times heads per key/value head) or more on average, 4-bit keys and values
+ * of d~ >= 32 are rounded to float16 as well (the tensor-core kernel for pieces of prompts).
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, ALIGNMENT, CUDA. */
 CCA_API int cca_paged_attention(const cca_paged_cache_t *cache, const cca_rows_t *q,
                                 const cca_rows_t *o, int n_heads, const int *cu_seqlens,
@@ -377,8 +382,9 @@ CCA_API size_t cca_decode_step_paged_workspace_size(const cca_config_t *cfg,
  * the layer's (a tensor-parallel rank's own heads), 16-bit pages CCA_F16 as the layer's latents.
  * conv_state and vshift_state are cca_cache_t's, for `batch` sequences.  lengths[b] counts the
  * tokens held BEFORE the step and is advanced by it; a sequence at max_pages * page_size is left
- * untouched, its y row is zero and CCA_ERR_CACHE_FULL recorded.  Every slot of the batch steps:
- * one whose sequence is shorter than its page table reaches needs that page to be its own.
+ * untouched, its y row is zero and CCA_ERR_CACHE_FULL recorded.  Every slot of the batch steps,
+ * so every slot's table names the page of its position lengths[b].  At most 8 query heads per
+ * key/value head, as cca_decode_step.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, ALIGNMENT, CUDA. */
 CCA_API int cca_decode_step_paged(const cca_config_t *cfg, const cca_weights_t *w, const void *x,
                                   void *y, const cca_paged_cache_t *cache, void *conv_state,

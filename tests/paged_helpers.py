@@ -81,7 +81,8 @@ class Batch:
 
         The tolerance, in the kernel's order of rounding:
           each weight is rounded to float16 (2^-11 of it), or to two bfloat16 terms (2^-16): as
-          much of sum_j p_j (|v_j| + |vz_j|), which bounds what the weights multiply;
+          much of sum_j p_j (|v_j| + |vz_j|), which bounds what the weights multiply (7.5 value
+          steps at most, centred codes);
           weights below float16's normal range keep an absolute 2^-25 beside a largest of at
           least 1 in 2^7 (value scales are brought there): 2^-27 per key of the largest value
           range, 2^-25 of the values at 16 bits;

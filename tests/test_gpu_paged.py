@@ -346,10 +346,83 @@ def test_attention_nonfinite_rows_stay_with_those_who_see_them(cuda_lib, bits):
         assert torch.isnan(o[6:]).any(-1).all()
 
 
+@pytest.mark.parametrize("bits,dtype", [(4, torch.float16), (16, torch.float16)])
+@pytest.mark.parametrize("B,Hkv,longest,page", [(300, 8, 400, 16), (200, 4, 200, 16), (129, 3, 700, 32), (4096, 1, 40, 64)])
+def test_attention_many_sequences(cuda_lib, bits, dtype, B, Hkv, longest, page):
+    """More items than warps, batches beyond one scan of a warp, the largest batch, tables so short
+    that no item is split; empty slots in between."""
+    cls = cuda_lib
+    rng = np.random.default_rng(B)
+    total = [int(x) for x in rng.integers(0, longest + 1, B)]
+    total[0], total[-1] = longest, 0
+    t = Batch(total, [1] * B, Hkv, 32, page, bits, dtype, seed=B)
+    q = t.rows(2 * Hkv)
+    cache = t.cache(cls)
+    o = cache.attend(q.cuda())
+    ref, tol = t.attention(q)
+    assert_within(o, ref, tol, f"{B} sequences")
+    cache.check()
+
+
+def test_attention_infinite_scale_behind_the_row(cuda_lib):
+    """A value scale of infinity in a later token's vector changes nothing for the tokens before it."""
+    cls = cuda_lib
+    t = Batch([70], [4], 1, 32, 16, 4, torch.float16, seed=7)
+    q = t.rows(2)
+    cache = t.cache(cls)
+    ref, tol = t.attention(q)
+    cache.scales[int(t.table[0, 68 // 16]), 0, 68 % 16, 2] = float("inf")
+    o = cache.attend(q.cuda())
+    assert_within(o[:2], ref[:2], tol[:2], "before it")
+    assert not torch.isfinite(o[2:]).any()
+
+
+def test_refusals_of_the_binding(cuda_lib):
+    cls = cuda_lib
+    t = Batch([20, 5], [1, 1], 2, 32, 16, 4, torch.float16)
+    c = t.cache(cls)
+    q, k = t.rows(4).cuda(), t.rows(2).cuda()
+    bad = [lambda: c.attend(q.cpu()), lambda: c.attend(q[..., :16]), lambda: c.attend(q.double()),
+           lambda: c.attend(q.view(1, 2, 4, 32)), lambda: c.attend(q, scale=0.0),
+           lambda: c.attend(q, cu_seqlens=torch.zeros(3, dtype=torch.int64, device="cuda")),
+           lambda: c.attend(q, cu_seqlens=torch.zeros(2, dtype=torch.int32, device="cuda")),
+           lambda: c.attend(q, out=q[:1]), lambda: c.append(k, k[:, :1]), lambda: c.append(k, k, q[:1]),
+           lambda: c.append(q, q), lambda: c.gather(), lambda: c.attend(q.transpose(-1, -2).contiguous().transpose(-1, -2)),
+           lambda: cls.PagedCache.from_pages(c.k, c.v, c.page_table, c.lengths),
+           lambda: cls.PagedCache.from_pages(c.k, c.v[:1], c.page_table, c.lengths, c.scales),
+           lambda: cls.PagedCache.from_pages(c.k, c.v, c.page_table.long(), c.lengths, c.scales),
+           lambda: cls.PagedCache.from_pages(c.k, c.v, c.page_table, c.lengths[:1], c.scales),
+           lambda: cls.PagedCache.from_pages(c.k, c.v, c.page_table, c.lengths, c.scales[..., :2])]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            print(i)
+    for f in (lambda: c.attend(t.rows(3).cuda()), lambda: c.append(k, k, rope_base=0.5),
+              lambda: c.attend(q, out=torch.empty(2, 1, 32, device="cuda").half().expand(2, 4, 32))):
+        with pytest.raises(cls.CCAError):
+            f()
+    c.check()
+
+
+def test_append_in_place_and_on_another_stream(cuda_lib):
+    cls = cuda_lib
+    t = Batch([20, 5], [1, 1], 2, 32, 16, 4, torch.float16)
+    a, b = t.cache(cls), t.cache(cls)
+    k, q = t.rows(2).cuda(), t.rows(4).cuda()
+    want = a.append(k, k, q, rope_base=BASE)
+    q2 = q.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = b.append(k, k, q2, rope_base=BASE, q_out=q2, stream=side)
+    side.synchronize()
+    assert got is q2 and torch.equal(q2, want) and torch.equal(a.k, b.k)
+
+
 # many rows a sequence: the tensor-core kernel (4 bits, d~ >= 32)
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("d,page,G", [(32, 16, 4), (64, 64, 4), (64, 16, 3), (128, 32, 8), (64, 32, 1)])
-@pytest.mark.parametrize("new,past", [((70, 300, 0, 1, 129), (0, 500, 9, 700, 33)), ((640, 3, 257), (1000, 0, 2))])
+@pytest.mark.parametrize("new,past", [((70, 300, 0, 1, 129), (0, 500, 9, 700, 33)), ((640, 3, 257), (1000, 0, 2)),
+                                      ((40, 60, 200) * 30, (10, 0, 150) * 30)])
 def test_attention_prompt_pieces(cuda_lib, dtype, d, page, G, new, past):
     """Ragged pieces beside single tokens and empty slots: row tiles and key tiles that end inside
     each other, runs that hold the end of one item and the start of the next."""
@@ -592,6 +665,26 @@ def test_layer_prefill_and_decode_over_pages(cuda_lib, dl, kv, bits):
             assert bf16_err(f64(y), f64(yd)) <= BF16_TOL
             assert torch.equal(paged.lengths, dense.lengths)
     paged.check()
+
+
+def test_tp_shares_over_pages(cuda_lib):
+    """Ranks of a tensor-parallel layer over their own pages: the shares add up to the layer's y."""
+    cls = cuda_lib
+    from compressed_latent_space_b200.tp import TPLayer
+    w = W.Workload("paged", 2, 30, 256, 4, 2, 2)
+    inp = W.make_inputs(w, seed=3, conv_std=0.4)
+    x = inp.x.cuda()
+    one = cls.CCALayer.from_workload(w, inp)
+    c1 = one.new_paged_cache(2, 2, 16, 16)
+    one.prefill(x[:, :29].contiguous(), cache=c1)
+    y = one.decode(x[:, 29].contiguous(), c1)
+    total = 0
+    for rank in range(2):
+        tp = TPLayer.from_workload(w, inp, 2, rank)
+        c = tp.new_paged_cache(2, 2, 16, 16)
+        tp.prefill_share(x[:, :29].contiguous(), cache=c)
+        total = total + tp.decode_share(x[:, 29].contiguous(), c).float()
+    assert bf16_err(f64(total), f64(y)) <= BF16_TOL
 
 
 def test_layer_paged_full_sequence_is_left_alone(cuda_lib):

@@ -43,7 +43,7 @@ BAD_PAGES = [
     (dict(batch=0), -1), (dict(max_pages=-1), -1), (dict(n_pages=0), -1), (dict(page_size=0), -1),
     (dict(n_kv_heads=0), -1), (dict(bits=8), -1), (dict(bits=16, dtype=0), -1),
     (dict(head_dim=48), -2), (dict(head_dim=256), -2), (dict(page_size=8), -2), (dict(page_size=24), -2),
-    (dict(page_size=8192), -2), (dict(max_pages=2 ** 21), -2), (dict(batch=4097), -2),
+    (dict(page_size=8192), -2), (dict(max_pages=2 ** 21), -2), (dict(batch=4097), -2), (dict(n_kv_heads=4097), -2),
     (dict(n_pages=2 ** 27), -2), (dict(n_pages=2 ** 26, n_kv_heads=2), -2), (dict(k=None), -1), (dict(scales=None), -1),
     (dict(page_table=None), -1), (dict(lengths=None), -1), (dict(k=(1 << 20) + 8), -5),
     (dict(scales=(1 << 20) + 2), -5),
@@ -76,7 +76,7 @@ def test_invalid_rows_are_refused(cls):
     assert app(k=rows(cls, ptr=(6 << 20) + 2)) == -5 and app(k=rows(cls, token_stride=60)) == -5
     assert app(k=rows(cls, head_stride=-32)) == -1
     assert app(k=rows(cls, seq_stride=68)) == -5
-    assert app(n=2 ** 26) == -2
+    assert app(n=2 ** 26) == -2 and app(k=rows(cls, head_stride=2 ** 31)) == -2
     # rows of an output that overlap
     big = dict(cu_seqlens=1 << 20)
     over = rows(cls, token_stride=16)
@@ -111,6 +111,8 @@ def test_launch_failure_is_reported(cls, monkeypatch):
     assert step(pg=pages(cls, n_kv_heads=4)) == -1 and step(pg=pages(cls, head_dim=64)) == -1
     assert step(pg=pages(cls, bits=16, scales=None, dtype=cls.CCA_BF16)) == -1
     assert step(cf=cls.make_config(256, 4, 2, 2, dtype=cls.CCA_F32)) == -2
+    many = pages(cls, n_kv_heads=1, head_dim=16)
+    assert step(pg=many, cf=cls.make_config(256, 16, 1, 1)) == -2        # 16 query heads on one
 
 
 def test_workspace_grows_with_the_machine_not_the_capacity(cls):
