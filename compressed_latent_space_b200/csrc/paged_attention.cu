@@ -694,15 +694,21 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
   static_assert(PIECE * 4 <= kStages * S::TILE, "a warp's ring holds a piece");
   extern __shared__ __align__(128) uint8_t smem[];
   int *pre = reinterpret_cast<int *>(smem + S::SMEM);          // [B + 1]
-  __shared__ int red[2][kWarps];
+  __shared__ int red[3][kWarps];
+  __shared__ PagedSeq seqs[32 * kWarps];             // the sequences, where there is a thread for each
   __shared__ PieceAt at_piece[kWarps][2];            // what each warp leaves in shared memory
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   pdl_wait();
   pdl_launch_dependents();                           // (after the wait: the merge relies on it)
   if (lane < 2) at_piece[warp][lane].state = kNone;
   const int B = p.batch.B;
-  int pad, upw;
-  {
+  int pad, upw, total;
+  const bool kept = B <= 32 * kWarps;
+  if (p.direct) {                                    // every sequence has Hkv items of one padded run
+    pad = p.whole;
+    total = B * p.Hkv * pad;
+    upw = pad * div(B * p.Hkv + p.warps - 1, p.by_warps);
+  } else {
     // the line's length and the number of items, then the padding, then the units before each
     // sequence; thread i takes a run of sequences (a single one up to 128: kept in registers)
     const int per = (B + 32 * kWarps - 1) / (32 * kWarps);
@@ -711,6 +717,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
     int tiles = 0, items = 0;
     for (int b = b0; b < b1; ++b) {
       mine = paged_seq(p.batch, b, p.status);
+      if (kept) seqs[b] = mine;
       const int rts = row_tiles(mine, R, p.G);
       items += rts;
       for (int rt = 0; rt < rts; ++rt) tiles += tiles_of<KT>(mine, rt, R, p.by_g);
@@ -759,14 +766,14 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
         const int x = __shfl_up_sync(0xffffffffu, inc, off);
         if (lane >= off) inc += x;
       }
-      __syncthreads();                               // red is read
-      if (lane == 31) red[0][warp] = inc;
+      int *part = red[attempt == 0 ? 2 : 0];         // (the first sums are read)
+      if (lane == 31) part[warp] = inc;
       __syncthreads();
       int run = inc - sum, all = 0;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) run += red[0][w];
-        all += red[0][w];
+        if (w < warp) run += part[w];
+        all += part[w];
       }
       if (attempt == 0 && few && all > static_cast<long long>(upw) * p.warps) {
         const int w = p.warps - items;
@@ -788,9 +795,9 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
         p.plan[B + 2] = pad;
       }
     }
+    total = pre[B];
   }
   const float rpad = rcp(pad);
-  const int total = pre[B];
   const int w = blockIdx.x * kWarps + warp;
   int u = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(w) * upw));
   const int uend = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(w + 1) * upw));
@@ -799,18 +806,27 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
   C core;
 
   while (u < uend) {
-    int b = 0;                                       // the last one with pre[b] <= u
-    for (int first = 0, n = B; n > 0;) {             // lanes probe [first, first + n) at 32 places
-      const int each = (n + 31) >> 5, i = first + lane * each;
-      const unsigned below = __ballot_sync(0xffffffffu, i < first + n && pre[min(i, B)] <= u);
-      first += (31 - __clz(below)) * each;           // (pre[first] <= u always)
-      n = each == 1 ? 0 : min(each, B - first);
-      b = first;
+    int b = 0, base, per_head;
+    PagedSeq s;
+    if (p.direct) {
+      b = div(u, p.by_seq);
+      per_head = pad;
+      base = b * p.Hkv * pad;
+      s = paged_seq(p.batch, b, p.status);
+    } else {
+      for (int first = 0, n = B; n > 0;) {           // the last b with pre[b] <= u: lanes probe
+        const int each = (n + 31) >> 5, i = first + lane * each;   // [first, first + n) at 32 places
+        const unsigned below = __ballot_sync(0xffffffffu, i < first + n && pre[min(i, B)] <= u);
+        first += (31 - __clz(below)) * each;         // (pre[first] <= u always)
+        n = each == 1 ? 0 : min(each, B - first);
+        b = first;
+      }
+      base = pre[b];
+      per_head = div(pre[b + 1] - base, p.by_hkv);
+      s = kept ? seqs[b] : paged_seq(p.batch, b, nullptr);
     }
-    const PagedSeq s = paged_seq(p.batch, b, nullptr);
-    const int per_head = div(pre[b + 1] - pre[b], p.by_hkv);
-    const int h = div(u - pre[b], per_head, rcp(per_head));
-    int t0 = u - pre[b] - h * per_head, rt = 0, T, TP;
+    const int h = div(u - base, per_head, rcp(per_head));
+    int t0 = u - base - h * per_head, rt = 0, T, TP;
     while (true) {
       T = tiles_of<KT>(s, rt, R, p.by_g);
       TP = padded(T, pad, rpad);
@@ -1167,6 +1183,8 @@ cudaError_t paged_attention(const PagedArgs &a, cudaStream_t st) {
   const bool tc = use_tc(a);
   p.warps = tc ? ctas : ctas * kWarps;
   p.by_warps = fast_div(static_cast<uint32_t>(p.warps));
+  p.direct = !tc && p.whole && !a.cu && a.tokens / a.B * p.G <= pick_rows(a);
+  p.by_seq = fast_div(static_cast<uint32_t>(p.direct ? a.Hkv * p.whole : 1));
   p.scale_log2 = static_cast<float>(a.scale * 1.4426950408889634);
   if (tc) return paged_attention_tc(a, &p, ctas, st);
   switch (a.D) {

@@ -33,6 +33,8 @@ struct AttnParams {
   int max_pages, n_pages, page_log2, Hkv, G, warps;
   FastDiv by_g, by_hkv, by_warps;
   int whole;                     // > 0: items are never split, none has more tiles than this
+  int direct;                    // ... and every sequence has one row tile: no plan is needed
+  FastDiv by_seq;                // units of a sequence then
   float scale_log2;
 };
 
