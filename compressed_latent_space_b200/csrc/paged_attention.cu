@@ -73,7 +73,7 @@ constexpr int ctas_by_regs(int d, int bits, int rows) {
   if (rows == 32) return 2;
   if (rows == 16) return d <= 32 ? 3 : 2;
   if (d == 128) return bits == 4 ? 3 : 2;
-  return bits == 4 && d <= 32 ? 5 : (bits == 16 && d == 64 ? 3 : 4);
+  return bits == 16 && d == 64 ? 3 : 4;
 }
 
 // 16-byte piece `c` of row `r` of a 16-bit tile, in pieces from the tile's start: an XOR order
@@ -1030,14 +1030,17 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
 }
 
 // Rows of a tile, by the rows of an average sequence: a tile's keys are read and unpacked once
-// for all its rows, and a 4-bit tile of fewer than 8 rows scores several key blocks at a time.
-// 16 at most at d~ = 128, where 32 rows' accumulators would not fit the registers.
+// for all its rows, and a 4-bit tile of fewer than 8 rows scores several key blocks at a time; but
+// 32 rows leave two warps a scheduler.  Measured, us a call, 16 / 32 rows a tile: 16 x 2048 keys of
+// 4 heads, 4 bits, d~ = 64: 64 rows 21.0 / 25.1, 128 rows 36.3 / 32.5; 8 x 2048 of 4, 16 bits, d~ = 32:
+// 48 rows 15.7 / 15.5, 64 rows 18.4 / 15.6.  16 at most at d~ = 128, where 32 rows' accumulators
+// would not fit the registers.
 int pick_rows(const PagedArgs &a) {
   const long long per = (static_cast<long long>(a.tokens) + a.B - 1) / a.B * (a.H / a.Hkv);
   if (a.bits == 4 && per <= 2) return 2;
   if (a.bits == 4 && per <= 4) return 4;
   if (per <= 8) return 8;
-  if (per <= 16 || a.D == 128) return 16;
+  if (per <= (a.bits == 4 ? 64 : 48) || a.D == 128) return 16;
   return 32;
 }
 
