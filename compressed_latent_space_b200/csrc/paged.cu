@@ -208,8 +208,10 @@ __global__ void __launch_bounds__(256, 4) paged_append_kernel(const __grid_const
         store8_as(p.qo.ptr, off, DT >= 0 ? DT : p.qo.dtype, lo8);
         store8_as(p.qo.ptr, off + HALF, DT >= 0 ? DT : p.qo.dtype, hi8);
       }
-      if (BITS == 16) continue;                      // (4 bits: other lanes may share in the extremes)
     }
+    // a row's lanes agree, and so does a warp but where it passes to the next rows; at 4 bits lanes
+    // without a key or value still take part in the extremes' exchange
+    if (BITS == 16 ? is_q : __all_sync(0xffffffffu, is_q)) continue;
     const int h = is_k ? row - p.HQ : row - kv0;
     const size_t slot = slot0 + (static_cast<size_t>(max(h, 0)) << p.page_log2);
     if constexpr (BITS == 16) {
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(const __grid_constant
   const int n = min(s.len, s.n);
   const int total = n * (2 * p.Hkv) * CPR;           // below 2^28 (the call's limit)
   const int stride = gridDim.x * blockDim.x;
-#pragma unroll 4
+#pragma unroll 1
   for (int e = blockIdx.x * blockDim.x + threadIdx.x; e < total; e += stride) {
     const int c0 = e % CPR * 16, row = e / CPR;
     const int i = div(row, p.by_rows), r = row - i * (2 * p.Hkv);
@@ -334,10 +336,11 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(const __grid_constant
     } else {
       const uint2 w = *reinterpret_cast<const uint2 *>(pages + slot * (D / 2) + c0 / 2);
       const float2 sz = __half22float2(p.scales[slot * 2 + which]);
+      // 2^23 + n, less 2^23; one rounding of scale n + zero
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        x[j] = __fadd_rn(__fmul_rn(static_cast<float>((w.x >> (4 * j)) & 15u), sz.x), sz.y);
-        y[j] = __fadd_rn(__fmul_rn(static_cast<float>((w.y >> (4 * j)) & 15u), sz.x), sz.y);
+        x[j] = fmaf(__uint_as_float(((w.x >> (4 * j)) & 15u) | 0x4b000000u) - 8388608.f, sz.x, sz.y);
+        y[j] = fmaf(__uint_as_float(((w.y >> (4 * j)) & 15u) | 0x4b000000u) - 8388608.f, sz.x, sz.y);
       }
     }
     store8_as(dst.ptr, off, dst.dtype, x);

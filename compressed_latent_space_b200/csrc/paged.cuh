@@ -110,10 +110,12 @@ __device__ __forceinline__ void store8_as(void *p, size_t off, int dtype, const 
   else store8(static_cast<__nv_bfloat16 *>(p) + off, v);
 }
 
+// (token and head strides fit 32 bits: one wide multiply each)
 __device__ __forceinline__ size_t row_offset(const Rows &r, bool packed, const PagedSeq &s, int b,
                                              int i, int h) {
-  const long long base = packed ? static_cast<long long>(s.t0) * r.tok : static_cast<long long>(b) * r.seq;
-  return static_cast<size_t>(base + static_cast<long long>(i) * r.tok + static_cast<long long>(h) * r.head);
+  const long long tok = static_cast<int>(r.tok), head = static_cast<int>(r.head);
+  const long long base = packed ? s.t0 * tok : b * r.seq;
+  return static_cast<size_t>(base + i * tok + h * head);
 }
 
 }  // namespace cca
