@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(256, 4) paged_append_kernel(const __grid_const
   pdl_launch_dependents();
   pdl_wait();
   const int heads = p.HQ + 2 * p.Hkv, kv0 = p.HQ + p.Hkv;
-  const int idx = blockIdx.x * blockDim.x + threadIdx.x;       // below 2^28 (the call's limit)
+  const int idx = blockIdx.x * blockDim.x + threadIdx.x;       // below 2^30 (the call's limit)
   const int c0 = idx % LPR * 8, unit = idx / LPR;
   const int group = div(unit, p.by_tokens), token = unit - group * p.batch.tokens;
   int row = group * p.rpt;
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(const __grid_constant
   const PagedSeq s = paged_seq(p.batch, b, p.status);
   const bool packed = p.batch.cu != nullptr;
   const int n = min(s.len, s.n);
-  const int total = n * (2 * p.Hkv) * CPR;           // below 2^28 (the call's limit)
+  const int total = n * (2 * p.Hkv) * CPR;           // below 2^30 (the call's limit)
   const int stride = gridDim.x * blockDim.x;
 #pragma unroll 1
   for (int e = blockIdx.x * blockDim.x + threadIdx.x; e < total; e += stride) {

@@ -47,7 +47,7 @@ int check_tokens(cca::PagedArgs &a, const int *cu, int tokens, int heads) {
   if (tokens < 0) return fail(CCA_ERR_INVALID_ARG, "tokens must be >= 0");
   if (!cu && tokens % a.B)
     return fail(CCA_ERR_INVALID_ARG, "%d tokens over a batch of %d need cu_seqlens", tokens, a.B);
-  if (static_cast<long long>(tokens) * heads >= (1LL << 31) / 128)
+  if (static_cast<long long>(tokens) * heads >= (1LL << 27))
     return fail(CCA_ERR_UNSUPPORTED, "%d tokens of %d rows each are too many for one call", tokens, heads);
   a.cu = cu;
   a.tokens = tokens;
@@ -193,6 +193,7 @@ CCA_API int cca_paged_attention(const cca_paged_cache_t *cache, const cca_rows_t
   if (tokens == 0) return ok();
   if ((rc = check_rows(a, "q", q, n_heads, false, a.q))) return rc;
   if ((rc = check_rows(a, "o", o, n_heads, true, a.qo))) return rc;
+  if (a.q.ptr == a.qo.ptr) return fail(CCA_ERR_INVALID_ARG, "q and o must not overlap");
   if (a.q.dtype == CCA_F32) return fail(CCA_ERR_UNSUPPORTED, "attention queries are CCA_F16 or CCA_BF16");
   if (a.bits == 16 && a.q.dtype != cache->dtype)
     return fail(CCA_ERR_INVALID_ARG, "queries of 16-bit pages have the pages' dtype");

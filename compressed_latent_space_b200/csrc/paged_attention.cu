@@ -39,7 +39,7 @@
 // whatever the values' scale.  2^e rides in the maximum (m holds the maximum less e), so that p,
 // its sum and all it weighs carry it, and it cancels.  16-bit pages: p itself in float16, or, for bfloat16 pages, as two
 // bfloat16 terms (one would keep 8 bits).  q . n: the queries in float16 times a power of two
-// that brings the warp's largest to 2^14 (exact but for elements 2^28 below it).
+// that brings the row's largest to 2^14 (exact but for elements 2^28 below it).
 //
 // Split: the tiles of all items in one line, cut into equal runs, one per warp; a warp walks its
 // run through a private ring of asynchronous copies, without any barrier.  Any mix of lengths is
@@ -169,7 +169,7 @@ struct Core {
 
   uint32_t qf[X][NT][KS][2];
   float qz[NT][2];               // scale_log2 * sum of the row's query (4 bits)
-  float ksf;                     // factor of a raw score into log2 units
+  uint64_t ksf[NT];              // factors of a row pair's raw scores into log2 units
   float m[NT][2], l[NT][2], z[NT][2];
   float o[MT][NT][4];
   float ws[NT][4];               // sums of the rounded weights (4 bits): [nt][col]
@@ -233,39 +233,41 @@ struct Core {
           put(nt, ks, 0, w[nt][2 * ks]);
           put(nt, ks, 1, w[nt][2 * ks + 1]);
         }
-      ksf = p.scale_log2;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) ksf[nt] = f2(p.scale_log2, p.scale_log2);
     } else {
-      float mxq = 0.f;
       auto val = [&](int nt, int i) {
         const uint32_t x = w[nt][i >> 1];
         const uint32_t hx = (i & 1) ? x >> 16 : x & 0xffffu;
         if constexpr (QBF16) return __uint_as_float(hx << 16);
         else return __half2float(__ushort_as_half(static_cast<unsigned short>(hx)));
       };
+      float fr[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float sum = 0.f;
+        float sum = 0.f, top = 0.f;
 #pragma unroll
         for (int i = 0; i < E; ++i) {
           const float x = val(nt, i);
-          mxq = fmaxf(mxq, fabsf(x));
+          top = fmaxf(top, fabsf(x));
           sum += x;
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         qz[nt][0] = __shfl_sync(0xffffffffu, sum, 8 * t) * p.scale_log2;
         qz[nt][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4) * p.scale_log2;
+        // 2^(14 - floor(log2 of the row's largest)), the exponent kept within what the inverse holds
+        const int e = max(-100, min(100, static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127));
+        fr[nt] = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+        const float back = __uint_as_float(static_cast<uint32_t>(24 - 14 + e + 127) << 23);
+        ksf[nt] = f2(p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t),
+                     p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t + 4));
       }
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1)
-        mxq = fmaxf(mxq, __shfl_xor_sync(0xffffffffu, mxq, off));
-      // 2^(14 - floor(log2 mxq)), the exponent kept within what the inverse below can hold
-      int e = static_cast<int>((__float_as_uint(mxq) >> 23) & 255u) - 127;
-      e = max(-100, min(100, e));
-      const float f = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23), f16 = f * 0.0625f;
-      ksf = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(24 - 14 + e + 127) << 23);
-#pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        const float f = fr[nt], f16 = f * 0.0625f;
         if constexpr (D == 16) {
           put(nt, 0, 0, pack_f16x2(val(nt, 0) * f, val(nt, 1) * f16));
           put(nt, 0, 1, pack_f16x2(val(nt, 2) * f, val(nt, 3) * f16));
@@ -470,19 +472,17 @@ struct Core {
           const float2 kk = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
           vzs[f][half] = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
           if (MASK && key0 + kf + 8 * half >= len) vzs[f][half] = make_float2(0.f, 0.f);   // no such key
-          vtop = fmaxf(vtop, vzs[f][half].x);
-          const float k = kk.x * ksf;
-          ks2 = f2(k, k);
+          vtop = fmaxf(vtop, fabsf(vzs[f][half].x));
+          ks2 = f2(kk.x, kk.x);
           kz2 = f2(kk.y, kk.y);
-        } else {
-          ks2 = f2(ksf, ksf);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           uint64_t off = f2(-m[nt][0], -m[nt][1]);
           if constexpr (BITS == 4) off = fma2(kz2, f2(qz[nt][0], qz[nt][1]), off);
           float x0, x1;
-          unf2(fma2(f2(c[f][nt][2 * half], c[f][nt][2 * half + 1]), ks2, off), x0, x1);
+          unf2(fma2(f2(c[f][nt][2 * half], c[f][nt][2 * half + 1]),
+                    BITS == 4 ? mul2(ks2, ksf[nt]) : ksf[nt], off), x0, x1);
           if (MASK) {
             if (key0 + kf + 8 * half >= lim[nt][0]) x0 = -INFINITY;
             if (key0 + kf + 8 * half >= lim[nt][1]) x1 = -INFINITY;

@@ -111,11 +111,18 @@ class CCALayer:
         c.vshift_state = torch.zeros(batch, max(self.n_kv - self.vshift_begin, 1), device=self.device)
         return c
 
+    def _check_paged(self, cache: PagedCache):
+        kc1 = self.cfg.conv_kernel - 1
+        conv = None if cache.conv_state is None else tuple(cache.conv_state.shape)
+        if (cache.vshift_state is None or cache.status is None
+                or conv != ((cache.batch, kc1, self.n_q + self.n_kv) if kc1 > 0 else None)
+                or cache.vshift_state.shape[1] != max(self.n_kv - self.vshift_begin, 1)):
+            raise ValueError("a layer's paged cache comes from its new_paged_cache")
+
     def _prefill_paged(self, x, cache: PagedCache, out, stream):
         # the forward over dense keys and values, which go on into the pages rotated already
         B, S, _ = x.shape
-        if cache.vshift_state is None or cache.status is None:
-            raise ValueError("a layer's paged cache comes from new_paged_cache")
+        self._check_paged(cache)
         if B != cache.batch or S > cache.max_pages * cache.page_size:
             raise ValueError(f"{B} x {S} tokens do not fit a paged cache of {cache.batch} x "
                              f"{cache.max_pages * cache.page_size}")
@@ -164,6 +171,9 @@ class CCALayer:
     def decode(self, x: torch.Tensor, cache: Cache | PagedCache, out: torch.Tensor | None = None,
                stream=None) -> torch.Tensor:
         if isinstance(cache, PagedCache):
+            self._check_paged(cache)
+            if x.shape != (cache.batch, self.cfg.d_model):
+                raise ValueError(f"x of {tuple(x.shape)} for a paged cache of {cache.batch} sequences")
             with cache._on(stream):
                 y = out if out is not None else torch.empty_like(x)
                 ws = torch.empty(cca_decode_step_paged_workspace_size(self.cfg, cache.struct),

@@ -3,7 +3,6 @@ C ABI: append with the rotation on the way, attention over the pages, dense read
 memory and marshals arguments only."""
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -108,9 +107,11 @@ class PagedCache:
 
     def _on(self, stream):
         """The device and, where given, the stream that a call's allocations belong to."""
-        if stream is not None:
-            return torch.cuda.stream(stream)
-        return torch.cuda.device(self.device)
+        if stream is None:
+            return torch.cuda.device(self.device)
+        if stream.device != self.device:
+            raise ValueError(f"a stream of {stream.device} for a cache on {self.device}")
+        return torch.cuda.stream(stream)
 
     # ------------------------------------------------------------------ the operators
     def append(self, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor | None = None,
@@ -119,7 +120,7 @@ class PagedCache:
         """Stores the new tokens' keys and values in their pages; with rope_base > 1 keys and
         queries are rotated to their positions on the way.  Returns the rotated queries."""
         if stream is not None:
-            with torch.cuda.stream(stream):
+            with self._on(stream):
                 return self.append(k, v, q, cu_seqlens, rope_base, q_out)
         r = self._call.append(self._desc, k, v, q, cu_seqlens, rope_base, q_out)
         if type(r) is int:
@@ -131,7 +132,7 @@ class PagedCache:
         """Causal attention of the new tokens' queries over their sequences' pages (which hold
         the new tokens already); scale None: 1 / sqrt(head_dim)."""
         if stream is not None:
-            with torch.cuda.stream(stream):
+            with self._on(stream):
                 return self.attend(q, cu_seqlens, scale, out)
         if scale is None:
             scale = 0.0
@@ -149,7 +150,7 @@ class PagedCache:
         cu_seqlens[b], or the given outputs (uniform rows of any strides; packed with
         cu_seqlens).  Rows behind a sequence's end are left as they are."""
         if stream is not None:
-            with torch.cuda.stream(stream):
+            with self._on(stream):
                 return self.gather(tokens, cu_seqlens, k_out, v_out, dtype)
         if (k_out is None) != (v_out is None) or (k_out is None and tokens is None):
             raise ValueError("gather takes k_out and v_out, or the number of tokens")

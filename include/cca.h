@@ -267,7 +267,7 @@ CCA_API int cca_cache_check(cca_cache_t *cache, void *stream);
  *               CCA_BF16); bits 4: [n_pages, n_kv_heads, page_size, head_dim / 2] bytes, channel
  *               2 j in the low and 2 j + 1 in the high half of byte j
  *   scales      bits 4: [n_pages, n_kv_heads, page_size, 4] float16: key scale, key zero, value
- *               scale, value zero of one token and head.  bits 16: NULL
+ *               scale, value zero of one token and head (scales >= 0).  bits 16: NULL
  *   page_table  [batch, max_pages] int32: page of tokens [i page_size, (i + 1) page_size) of a
  *               sequence; entries past a sequence's tokens are not read
  *   lengths     [batch] int32: tokens of each sequence, the new tokens of the call INCLUDED
@@ -275,7 +275,7 @@ CCA_API int cca_cache_check(cca_cache_t *cache, void *stream);
  *               holds no sequence: nothing is stored for it and its output rows are zero
  *   status      int32 sticky error word, or NULL; read and cleared by cca_paged_check
  * head_dim in {16, 32, 64, 128}; page_size a power of two in [16, 4096]; max_pages * page_size
- * <= 2^24; batch and n_kv_heads <= 4096; n_pages * n_kv_heads * page_size < 2^31; at most 2^24
+ * <= 2^24; batch and n_kv_heads <= 4096; n_pages * n_kv_heads * page_size < 2^31; at most 2^27
  * (token, head) rows a call.  Two sequences may share pages they only read; rows behind a sequence's length are never read as data and may hold
  * anything.
  *
@@ -355,7 +355,7 @@ CCA_API size_t cca_paged_attention_workspace_size(const cca_paged_cache_t *cache
  * 0 .. lengths[b] - n + i; query head h reads key/value head h / (n_heads / n_kv_heads), as the
  * layer's attention (gist.science/de explainer, 2. Methodik; Extension: CCGQA).
  *   o = softmax(scale q k^T) v       (scale 0: 1 / sqrt(head_dim))
- * q is CCA_F16 or CCA_BF16 (at 16 bits the pages' type), o any type.  A query that sees no key
+ * q is CCA_F16 or CCA_BF16 (at 16 bits the pages' type), o any type; they must not overlap.  A query that sees no key
  * (length 0, or a position below 0) gets a row of zeros.  An infinity or NaN in a cached row
  * reaches the rows that see it; at 16 bits a value's may also reach the new tokens before it
  * of the same sequence and call.

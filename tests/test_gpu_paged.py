@@ -377,6 +377,21 @@ def test_attention_infinite_scale_behind_the_row(cuda_lib):
     assert not torch.isfinite(o[2:]).any()
 
 
+def test_attention_rows_do_not_disturb_each_other(cuda_lib):
+    """An infinite, a NaN and a huge query head beside ordinary ones (4 bits: the queries' power of
+    two is each row's own)."""
+    cls = cuda_lib
+    for n, d in ((1, 32), (5, 64), (60, 64)):
+        t = Batch([300], [n], 1, d, 16, 4, torch.bfloat16, seed=9)
+        q = t.rows(8)
+        clean = t.cache(cls).attend(q.cuda())
+        q[:, 1, 3], q[:, 2, 5], q[:, 3] = float("inf"), float("nan"), q[:, 3] * 1e30
+        o = t.cache(cls).attend(q.cuda())
+        keep = [0, 4, 5, 6, 7]
+        assert torch.equal(o[:, keep], clean[:, keep])
+        assert torch.isnan(o[:, 1]).all() and torch.isnan(o[:, 2]).all()
+
+
 def test_refusals_of_the_binding(cuda_lib):
     cls = cuda_lib
     t = Batch([20, 5], [1, 1], 2, 32, 16, 4, torch.float16)
@@ -397,7 +412,7 @@ def test_refusals_of_the_binding(cuda_lib):
         with pytest.raises(ValueError):
             f()
             print(i)
-    for f in (lambda: c.attend(t.rows(3).cuda()), lambda: c.append(k, k, rope_base=0.5),
+    for f in (lambda: c.attend(t.rows(3).cuda()), lambda: c.attend(q, out=q), lambda: c.append(k, k, rope_base=0.5),
               lambda: c.attend(q, out=torch.empty(2, 1, 32, device="cuda").half().expand(2, 4, 32))):
         with pytest.raises(cls.CCAError):
             f()
@@ -685,6 +700,21 @@ def test_tp_shares_over_pages(cuda_lib):
         tp.prefill_share(x[:, :29].contiguous(), cache=c)
         total = total + tp.decode_share(x[:, 29].contiguous(), c).float()
     assert bf16_err(f64(total), f64(y)) <= BF16_TOL
+
+
+def test_layer_refuses_another_layers_pages(cuda_lib):
+    cls = cuda_lib
+    w = W.Workload("paged", 2, 32, 256, 4, 2, 2)
+    layer = cls.CCALayer.from_workload(w, W.make_inputs(w))
+    w2 = W.Workload("paged", 2, 32, 512, 8, 2, 2)
+    other = cls.CCALayer.from_workload(w2, W.make_inputs(w2)).new_paged_cache(2, 2, 16)
+    x = torch.zeros(2, 256, dtype=torch.bfloat16, device="cuda")
+    mine = layer.new_paged_cache(2, 2, 16)
+    for f in (lambda: layer.decode(x, other), lambda: layer.prefill(x[:, None], cache=other),
+              lambda: layer.decode(x[:1], mine), lambda: layer.decode(x, cls.PagedCache(2, 2, 16, 2, 32)),
+              lambda: layer.prefill(x[:, None].expand(2, 40, 256).contiguous(), cache=mine)):
+        with pytest.raises(ValueError):
+            f()
 
 
 def test_layer_paged_full_sequence_is_left_alone(cuda_lib):

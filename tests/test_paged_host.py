@@ -78,13 +78,14 @@ def test_invalid_rows_are_refused(cls):
     assert app(k=rows(cls, seq_stride=68)) == -5
     assert app(n=2 ** 26) == -2 and app(k=rows(cls, head_stride=2 ** 31)) == -2
     # rows of an output that overlap
-    big = dict(cu_seqlens=1 << 20)
     over = rows(cls, token_stride=16)
     assert app(q=r, qo=over, H=4, cu=1 << 20) == -1
     assert app(q=r, qo=rows(cls, head_stride=0), H=4) == -1
     assert app(q=r, qo=rows(cls, seq_stride=0), H=4) == -1
     assert call(cls, "cca_paged_gather", p, rows(cls, head_stride=16), r, None, 2, None) == -1
-    att = lambda q=r, o=r, H=4, n=2, scale=0.0, ws=1 << 20, nb=1 << 30, pg=p: call(
+    out = rows(cls, ptr=7 << 20)
+    assert call(cls, "cca_paged_attention", p, r, r, 4, None, 2, 0.0, 1 << 20, 1 << 30, None) == -1   # q is o
+    att = lambda q=r, o=out, H=4, n=2, scale=0.0, ws=1 << 20, nb=1 << 30, pg=p: call(
         cls, "cca_paged_attention", pg, q, o, H, None, n, scale, ws, nb, None)
     assert att(H=3) == -1 and att(H=0) == -1 and att(q=None) == -1 and att(o=None) == -1
     assert att(scale=float("inf")) == -1 and att(scale=float("nan")) == -1
@@ -100,7 +101,7 @@ def test_launch_failure_is_reported(cls, monkeypatch):
     assert call(cls, "cca_paged_append", p, None, r, r, None, 0, None, 2, 0.0, None) == -6
     assert call(cls, "cca_paged_gather", p, r, r, None, 2, None) == -6
     assert call(cls, "cca_paged_attention", p, rows(cls, seq_stride=128, token_stride=128),
-                rows(cls, seq_stride=128, token_stride=128), 4, None, 2, 0.0, 1 << 20, 1 << 30, None) == -6
+                rows(cls, ptr=7 << 20, seq_stride=128, token_stride=128), 4, None, 2, 0.0, 1 << 20, 1 << 30, None) == -6
     cfg, w = cls.make_config(256, 4, 2, 2), cls.cca_weights_t(1 << 20, 1 << 20, 1 << 20, 1 << 20)
     n = cls.cca_decode_step_paged_workspace_size(cfg, p)
     assert n > 0
