@@ -10,8 +10,11 @@
 // than the range's ends.  Every step is the IEEE one (division, no contraction), so the same
 // input gives the same codes everywhere.
 //
-// Both kernels move each byte once; HBM bounds them at long prompts and launch latency at single
-// tokens.
+// Both kernels move each byte once.  On one B200: 2 x 16384 tokens of 16 query, 4 key and 4 value
+// heads, d~ = 64, 16 bits, 41 us (4.9 TB/s, 75 % of the measured copy rate); 4 x 4096 tokens of
+// 16 + 16 + 16, d~ = 32, 4 bits, 25 us for the append (bound by issue slots: codes and extremes) and
+// 15 us for the read-back (44 MB; bound by its loads' latency, four places at a time measured the
+// same); one token of each of 64 sequences 2.7 us, launch latency.
 #include "paged.cuh"
 
 namespace cca {

