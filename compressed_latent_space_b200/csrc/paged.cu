@@ -388,7 +388,19 @@ cudaError_t paged_append(const PagedArgs &a, cudaStream_t st) {
   p.groups = (heads + p.rpt - 1) / p.rpt;
   p.by_tokens = fast_div(static_cast<uint32_t>(a.tokens));
   p.rotate = a.rope_base > 0.f;
-  rope_turns_host(a.D, p.rotate ? a.rope_base : 2.0, p.turn_hi, p.turn_lo, 64);
+  if (p.rotate) {
+    // base^(-2 i / d) / 2 pi by a running product in long double (64 pow() calls are 3 us of a call
+    // whose kernel takes 2), as rope_turns_host's hi + lo pairs
+    const long double step = powl(static_cast<long double>(a.rope_base), -2.0L / a.D);
+    long double t = 1.0L / 6.283185307179586476925L;
+    for (int i = 0; i < a.D / 2; ++i, t *= step) {
+      const double turns = static_cast<double>(t);
+      p.turn_hi[i] = static_cast<float>(turns);
+      p.turn_lo[i] = static_cast<float>(turns - static_cast<double>(p.turn_hi[i]));
+    }
+  } else {
+    for (int i = 0; i < a.D / 2; ++i) p.turn_hi[i] = p.turn_lo[i] = 0.f;
+  }
 #define CCA_APPEND(DD)                                                                  \
   if (a.D == DD)                                                                        \
     return a.bits == 4 ? launch_append<DD, 4>(a, p, st) : launch_append<DD, 16>(a, p, st);

@@ -2,8 +2,9 @@
 // zero per vector), for any number of new tokens per sequence and ragged lengths.
 //
 // Row r = i G + (h - g G) of sequence b and key/value head g is token i's query head h; its
-// token sits at position len - n + i and sees the keys up to there.  Rows are taken R at a time; a work item is (sequence, head, row tile) and its units are the tiles of KT keys that
-// its last row sees.
+// token sits at position len - n + i and sees the keys up to there.  Rows are taken R at a time; a
+// work item is (sequence, head, row tile) and its units are the tiles of KT keys that its last row
+// sees.
 //
 // Mathematics, 4 bits (k_j = ks_j n_j + kz_j, v_j = vs_j u_j + vz_j with codes n, u in 0..15):
 //   s_j = c (q . k_j) = (c ks_j) (q . n_j) + kz_j (c sum q)
@@ -13,9 +14,9 @@
 // of the rounded part again (one more row of the product, of ones, sums w~):
 //   o   = sum_j w~_j u_j - 7.5 sum_j w~_j + sum_j p_j (vz_j + 7.5 vs_j)
 // (error against 64 bits at 8k keys 5.1e-4 without, 3.0e-4 with it, 2.1e-4 of that the result's
-// own rounding, for 3 % of the time).  So the tensor cores multiply by the bare codes and the scales are applied to one score per
-// (key, row) instead of d~ channels.  A code needs no conversion either: n in the low bits of a
-// float16 is the subnormal n 2^-24, and four bits further up n 2^-20, so `word & 0x000f000f` and
+// own rounding, for 3 % of the time).  So the tensor cores multiply by the bare codes and the scales
+// are applied to one score per (key, row) instead of d~ channels.  A code needs no conversion
+// either: n in the low bits of a float16 is the subnormal n 2^-24, and four bits further up n 2^-20, so `word & 0x000f000f` and
 // `word & 0x00f000f0` are pairs of operands, exact, and the powers of two go into the queries
 // (those that meet the second kind are scaled by 1/16) and into the result.
 //
@@ -37,9 +38,9 @@
 // units), so p <= 2^8; sums in float32.  4 bits: p vs is rounded to float16, for which a power of
 // two 2^e (per warp, following the largest vs met) brings vs under 2^7: 11 bits of each weight
 // whatever the values' scale.  2^e rides in the maximum (m holds the maximum less e), so that p,
-// its sum and all it weighs carry it, and it cancels.  16-bit pages: p itself in float16, or, for bfloat16 pages, as two
-// bfloat16 terms (one would keep 8 bits).  q . n: the queries in float16 times a power of two
-// that brings the row's largest to 2^14 (exact but for elements 2^28 below it).
+// its sum and all it weighs carry it, and it cancels.  16-bit pages: p itself in float16, or, for
+// bfloat16 pages, as two bfloat16 terms (one would keep 8 bits).  q . n: the queries in float16
+// times a power of two that brings the row's largest to 2^14 (exact but for elements 2^28 below it).
 //
 // Split: the tiles of all items in one line, cut into equal runs, one per warp; a warp walks its
 // run through a private ring of asynchronous copies, without any barrier.  Any mix of lengths is

@@ -71,10 +71,14 @@ class PagedCache:
     def _take(self, k, v, table, lengths, scales, status):
         self._call = bind = _native()
         self._desc = bind.describe(k, v, table, lengths, scales, status)
-        self.device = k.device
         self.k, self.v, self.scales = k, v, scales
         self.page_table, self.lengths, self.status = table, lengths, status
-        self.conv_state = self.vshift_state = None     # a layer's (CCALayer.new_paged_cache)
+
+    conv_state = vshift_state = None                   # a layer's (CCALayer.new_paged_cache)
+
+    @property
+    def device(self) -> torch.device:
+        return self.k.device
 
     @property
     def struct(self) -> cca_paged_cache_t:
