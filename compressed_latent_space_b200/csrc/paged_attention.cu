@@ -16,9 +16,10 @@
 // (error against 64 bits at 8k keys 5.1e-4 without, 3.0e-4 with it, 2.1e-4 of that the result's
 // own rounding, for 3 % of the time).  So the tensor cores multiply by the bare codes and the scales
 // are applied to one score per (key, row) instead of d~ channels.  A code needs no conversion
-// either: n in the low bits of a float16 is the subnormal n 2^-24, and four bits further up n 2^-20, so `word & 0x000f000f` and
-// `word & 0x00f000f0` are pairs of operands, exact, and the powers of two go into the queries
-// (those that meet the second kind are scaled by 1/16) and into the result.
+// either: n in the low bits of a float16 is the subnormal n 2^-24, and four bits further up
+// n 2^-20, so `word & 0x000f000f` and `word & 0x00f000f0` are pairs of operands, exact, and the
+// powers of two go into the queries (those that meet the second kind are scaled by 1/16) and into
+// the result.
 //
 // Both products are m16n8k16 with the keys (resp. the channels) on the 16 side and eight rows on
 // the 8 side: S^T = K Q^T and O^T = V^T P^T.  That way the usual 1 to 8 query heads of a group

@@ -111,18 +111,30 @@ class CCALayer:
         c.vshift_state = torch.zeros(batch, max(self.n_kv - self.vshift_begin, 1), device=self.device)
         return c
 
-    def _check_paged(self, cache: PagedCache):
+    def _check_paged(self, cache: PagedCache, x: torch.Tensor, out: torch.Tensor | None):
+        dev = self.w_qkv.device
+
+        def is_state(t, *shape):
+            return (t is not None and tuple(t.shape) == shape and t.dtype == torch.float32
+                    and t.device == dev and t.is_contiguous())
+
         kc1 = self.cfg.conv_kernel - 1
-        conv = None if cache.conv_state is None else tuple(cache.conv_state.shape)
-        if (cache.vshift_state is None or cache.status is None
-                or conv != ((cache.batch, kc1, self.n_q + self.n_kv) if kc1 > 0 else None)
-                or cache.vshift_state.shape[1] != max(self.n_kv - self.vshift_begin, 1)):
+        conv, shift = cache.conv_state, cache.vshift_state
+        if (cache.device != dev or cache.status is None
+                or not (is_state(conv, cache.batch, kc1, self.n_q + self.n_kv) if kc1 > 0 else conv is None)
+                or not is_state(shift, cache.batch, max(self.n_kv - self.vshift_begin, 1))):
             raise ValueError("a layer's paged cache comes from its new_paged_cache")
+        for name, t in (("x", x), ("out", x if out is None else out)):
+            if (t.shape != x.shape or t.dtype != self.dtype or t.device != dev
+                    or not t.is_contiguous()):
+                raise ValueError(f"{name}: a contiguous {self.dtype} tensor of x's shape on {dev} expected")
 
     def _prefill_paged(self, x, cache: PagedCache, out, stream):
         # the forward over dense keys and values, which go on into the pages rotated already
+        if x.dim() != 3 or x.shape[2] != self.cfg.d_model:
+            raise ValueError(f"x of {tuple(x.shape)} for a layer of width {self.cfg.d_model}")
+        self._check_paged(cache, x, out)
         B, S, _ = x.shape
-        self._check_paged(cache)
         if B != cache.batch or S > cache.max_pages * cache.page_size:
             raise ValueError(f"{B} x {S} tokens do not fit a paged cache of {cache.batch} x "
                              f"{cache.max_pages * cache.page_size}")
@@ -171,7 +183,7 @@ class CCALayer:
     def decode(self, x: torch.Tensor, cache: Cache | PagedCache, out: torch.Tensor | None = None,
                stream=None) -> torch.Tensor:
         if isinstance(cache, PagedCache):
-            self._check_paged(cache)
+            self._check_paged(cache, x, out)
             if x.shape != (cache.batch, self.cfg.d_model):
                 raise ValueError(f"x of {tuple(x.shape)} for a paged cache of {cache.batch} sequences")
             with cache._on(stream):

@@ -10,6 +10,7 @@ import torch
 from . import _check, cca_paged_cache_t, cca_paged_check, load
 
 _bind = None
+_REGIONS = ("k", "v", "page_table", "lengths", "scales", "status")
 
 
 def _native():
@@ -34,8 +35,8 @@ class PagedCache:
     tokens, 16 bits (float16 or bfloat16) or 4 (codes with a float16 scale and zero per vector).
 
     ``page_table`` [batch, max_pages] and ``lengths`` [batch] (int32, on the device) are the
-    caller's to fill: lengths count the tokens of the call they are passed to, its new ones
-    included.  With ``n_pages`` None every sequence owns ``max_pages`` pages and the table says
+    caller's to fill or to replace: lengths count the tokens of the call they are passed to, its
+    new ones included.  With ``n_pages`` None every sequence owns ``max_pages`` pages and the table says
     so; otherwise the table starts at zero.
 
     New tokens come as [tokens, heads, d] with ``cu_seqlens`` (int32 [batch + 1] on the device),
@@ -70,9 +71,17 @@ class PagedCache:
 
     def _take(self, k, v, table, lengths, scales, status):
         self._call = bind = _native()
-        self._desc = bind.describe(k, v, table, lengths, scales, status)
+        desc = bind.describe(k, v, table, lengths, scales, status)
         self.k, self.v, self.scales = k, v, scales
         self.page_table, self.lengths, self.status = table, lengths, status
+        self._desc = desc
+
+    def __setattr__(self, name, value):
+        # calls take the addresses in _desc: a tensor put in another's place has to get there
+        if name in _REGIONS and "_desc" in self.__dict__:
+            now = {n: value if n == name else getattr(self, n) for n in _REGIONS}
+            object.__setattr__(self, "_desc", self._call.describe(*now.values()))
+        object.__setattr__(self, name, value)
 
     conv_state = vshift_state = None                   # a layer's (CCALayer.new_paged_cache)
 

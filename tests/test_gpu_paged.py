@@ -717,6 +717,45 @@ def test_layer_refuses_another_layers_pages(cuda_lib):
             f()
 
 
+def test_layer_refuses_misplaced_states_and_rows(cuda_lib):
+    cls = cuda_lib
+    w = W.Workload("paged", 2, 32, 256, 4, 2, 2)
+    layer = cls.CCALayer.from_workload(w, W.make_inputs(w))
+    x = torch.zeros(2, 256, dtype=torch.bfloat16, device="cuda")
+    for name in ("conv_state", "vshift_state"):
+        for spoil in (lambda t: t[:1], lambda t: t.cpu(), lambda t: t.half(), lambda t: None,
+                      lambda t: t.repeat_interleave(2, -1)[..., ::2]):
+            c = layer.new_paged_cache(2, 2, 16)
+            setattr(c, name, spoil(getattr(c, name)))
+            for f in (lambda: layer.decode(x, c), lambda: layer.prefill(x[:, None], cache=c)):
+                with pytest.raises(ValueError):
+                    f()
+    c = layer.new_paged_cache(2, 2, 16)
+    wide = torch.zeros(2, 512, dtype=torch.bfloat16, device="cuda")
+    for bad in (x.float(), x.cpu(), wide[:, ::2], wide):
+        for f in (lambda: layer.decode(bad, c), lambda: layer.prefill(bad[:, None], cache=c),
+                  lambda: layer.decode(x, c, out=bad),
+                  lambda: layer.prefill(x[:, None], cache=c, out=bad[:, None])):
+            with pytest.raises(ValueError):
+                f()
+    assert c.lengths.tolist() == [0, 0]
+
+
+def test_replaced_lengths_and_table_are_used(cuda_lib):
+    cls = cuda_lib
+    g = torch.Generator().manual_seed(5)
+    c = cls.PagedCache(2, 2, 16, 2, 32, 16)
+    k, v = (torch.randn(2, 9, 2, 32, generator=g).half().cuda() for _ in range(2))
+    c.lengths = torch.full((2,), 9, dtype=torch.int32, device="cuda")
+    c.page_table = torch.tensor([[3, 0], [1, 2]], dtype=torch.int32, device="cuda")
+    c.append(k, v)
+    assert torch.equal(c.k[3, :, :9], k[0].transpose(0, 1))
+    assert torch.equal(c.v[1, :, :9], v[1].transpose(0, 1))
+    kd, vd = c.gather(18)
+    assert torch.equal(kd.view(2, 9, 2, 32), k) and torch.equal(vd.view(2, 9, 2, 32), v)
+    c.check()
+
+
 def test_layer_paged_full_sequence_is_left_alone(cuda_lib):
     cls = cuda_lib
     w = W.Workload("paged", 2, 32, 256, 4, 2, 2)

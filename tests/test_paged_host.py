@@ -158,3 +158,25 @@ def test_oracle_agrees_with_the_layer_oracle():
     # a query before the first key
     o, _, _ = P.attention(x, k[:3], v[:3], 1.0)
     assert (o[:2] == 0).all() and (o[2] != 0).any()
+
+
+def test_replaced_tensors_reach_the_calls(cls):
+    import torch
+    c = cls.PagedCache(2, 3, 16, 2, 16, 4, device="cpu")
+    for name in ("k", "v", "page_table", "lengths", "scales", "status"):
+        t = getattr(c, name).clone()
+        setattr(c, name, t)
+        assert getattr(c, name) is t
+        assert getattr(c.struct, name) == t.data_ptr()
+    c.lengths += 1
+    assert c.lengths.tolist() == [1, 1] and c.struct.lengths == c.lengths.data_ptr()
+    before, desc = c.lengths, bytes(c.struct)
+    for bad in (torch.zeros(3, dtype=torch.int32), torch.zeros(2), None,
+                torch.zeros(4, dtype=torch.int32)[::2]):
+        with pytest.raises(ValueError):
+            c.lengths = bad
+        assert c.lengths is before and bytes(c.struct) == desc
+    c.status = None
+    assert not c.struct.status
+    c.page_table = torch.zeros(2, 5, dtype=torch.int32)
+    assert c.max_pages == 5 and c.struct.max_pages == 5
