@@ -50,7 +50,8 @@ struct PagedSeq {
 // A sequence whose row range leaves [0, tokens] has no new rows here, one that would pass its
 // pages' capacity holds nothing; both are reported.  len < n (a slot without a sequence has
 // len = 0) leaves the first new positions negative: they see no key and are not stored.
-__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch &p, int b, int *status) {
+// *odd is set for a row range that leaves [0, tokens] or runs backwards.
+__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch &p, int b, int *status, bool *odd = nullptr) {
   PagedSeq s;
   if (p.cu) {
     s.t0 = p.cu[b];
@@ -58,6 +59,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatch &p, int b, int *s
     s.n = t1 - s.t0;
     if (s.t0 < 0 || t1 < s.t0 || t1 > p.tokens) {
       report(status, DEV_LAYOUT);
+      if (odd) *odd = true;
       s.t0 = s.n = 0;
     }
   } else {

@@ -723,8 +723,9 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
     PagedSeq mine = {0, 0, 0};
     int tiles = 0, items = 0;
+    bool odd = false;
     for (int b = b0; b < b1; ++b) {
-      mine = paged_seq(p.batch, b, p.status);
+      mine = paged_seq(p.batch, b, p.status, &odd);
       if (kept) seqs[b] = mine;
       const int rts = row_tiles(mine, R, p.G);
       items += rts;
@@ -735,12 +736,13 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
       red[0][warp] = wt;
       red[1][warp] = wi;
     }
-    __syncthreads();
+    // (the host bounds the units of as many rows as the call has: with more, nothing is computed)
+    const bool none = __syncthreads_or(odd) && paged_overlap(p.batch);
     tiles = items = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      tiles += red[0][w];
-      items += red[1][w];
+      tiles += none ? 0 : red[0][w];
+      items += none ? 0 : red[1][w];
     }
     tiles *= p.Hkv;
     items *= p.Hkv;
@@ -761,7 +763,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_by_regs(D, BITS, R)) paged_a
       int sum = 0;
       for (int b = b0; b < b1; ++b) {
         if (per > 1) mine = paged_seq(p.batch, b, nullptr);
-        const int rts = row_tiles(mine, R, p.G);
+        const int rts = none ? 0 : row_tiles(mine, R, p.G);
         int u = 0;
         for (int rt = 0; rt < rts; ++rt) u += padded(tiles_of<KT>(mine, rt, R, p.by_g), pad, rpad);
         u *= p.Hkv;

@@ -44,6 +44,15 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Whether the sequences have more rows between them than the call.  Ranges that all run forwards
+// in [0, tokens] cannot (each begins where the one before ends), so only a batch with an odd one is
+// counted.
+__device__ __noinline__ bool paged_overlap(const PagedBatch &p) {
+  long long n = 0;
+  for (int b = 0; b < p.B; ++b) n += paged_seq(p, b, nullptr).n;
+  return n > p.tokens;
+}
+
 // Tiles of keys that the rows of row tile rt see; one even where there is none, so that some
 // warp writes the rows.
 template <int KT>
@@ -129,6 +138,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
   pdl_launch_dependents();
   if (h >= p.Hkv || rr0 >= rows) return;
   const int p0 = p.plan[b], p1 = p.plan[b + 1], upw = p.plan[p.batch.B + 1], pad = p.plan[p.batch.B + 2];
+  if (p0 == p1) return;                              // overlapping sequences: nothing was computed
   const float rpad = rcp(pad), rrun = rcp(upw * RUNS);
   int u0 = p0 + h * div(p1 - p0, p.by_hkv);
   for (int rt = 0; rt < rts; ++rt) {

@@ -157,8 +157,9 @@ __global__ void __launch_bounds__(32 * TC_WARPS, 1) paged_tc_kernel(const __grid
     const int per = (B + 32 * TC_WARPS - 1) / (32 * TC_WARPS);
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
     int sum = 0;
+    bool odd = false;
     for (int b = b0; b < b1; ++b) {
-      const PagedSeq s = paged_seq(p.batch, b, p.status);
+      const PagedSeq s = paged_seq(p.batch, b, p.status, &odd);
       const int rts = row_tiles(s, TC_ROWS, p.G);
       int u = 0;
       for (int rt = 0; rt < rts; ++rt) u += tiles_of<TN>(s, rt, TC_ROWS, p.by_g);
@@ -172,12 +173,13 @@ __global__ void __launch_bounds__(32 * TC_WARPS, 1) paged_tc_kernel(const __grid
       if (lane >= off) inc += x;
     }
     if (lane == 31) bars.red[warp] = inc;
-    __syncthreads();
-    int run = inc - sum;
-    for (int w = 0; w < warp; ++w) run += bars.red[w];
+    // (the host bounds the units of as many rows as the call has: with more, nothing is computed)
+    const bool none = __syncthreads_or(odd) && paged_overlap(p.batch);
+    int run = none ? 0 : inc - sum;
+    for (int w = 0; w < warp && !none; ++w) run += bars.red[w];
     if (tid == 0) pre[0] = 0;
     for (int b = b0; b < b1; ++b) {
-      run += pre[b + 1];
+      run += none ? 0 : pre[b + 1];
       pre[b + 1] = run;
     }
   }

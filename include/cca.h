@@ -286,9 +286,10 @@ CCA_API int cca_cache_check(cca_cache_t *cache, void *stream);
  *
  * Kernel-side errors leave the status word set and touch nothing out of range: CCA_ERR_PAGE (an
  * entry outside [0, n_pages): its tokens are not stored and read as zeros; or cu_seqlens that
- * leave [0, tokens], or a negative length: that sequence is taken as empty), CCA_ERR_CACHE_FULL
- * (a length beyond max_pages * page_size: taken as empty), CCA_ERR_RANGE (a value beyond
- * float16 stored, float16 pages and 4 bits). */
+ * leave [0, tokens] or run backwards, or a negative length: that sequence is taken as empty, and
+ * attention computes nothing where the others then overlap to more than the call's rows),
+ * CCA_ERR_CACHE_FULL (a length beyond max_pages * page_size: taken as empty), CCA_ERR_RANGE (a
+ * value beyond float16 stored, float16 pages and 4 bits). */
 typedef struct {
   void *k;
   void *v;

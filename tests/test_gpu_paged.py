@@ -560,6 +560,32 @@ def test_full_and_invalid_sequences(cuda_lib):
             assert (out[1] == 3).all()
 
 
+@pytest.mark.parametrize("bits,d", [(4, 16), (4, 64), (16, 32)])
+def test_overlapping_sequences_compute_nothing(cuda_lib, bits, d):
+    """Row ranges of which one runs backwards and the others have more rows than the call: few
+    rows, many, and units (rows x keys) beyond 32 bits between them."""
+    cls = cuda_lib
+    for B, pages, n, length in ((4, 8, 3, 40), (4, 8, 200, 512), (256, 2 ** 14, 2 ** 17, 2 ** 20)):
+        cache = cls.PagedCache(B, pages, 64, 2, d, bits, n_pages=1)
+        cache.lengths.fill_(length)
+        q = torch.ones(n, 8, d, dtype=torch.float16, device="cuda")
+        cu = torch.tensor([0, n] * (B // 2) + [0], dtype=torch.int32, device="cuda")
+        out = torch.full_like(q, 3.0)
+        cache.attend(q, cu_seqlens=cu, out=out)
+        with pytest.raises(cls.CCAError) as e:
+            cache.check()
+        assert e.value.code == cls.CCA_ERR_PAGE
+        assert (out == 3).all()
+    # two sequences on the same rows, one row short of too many: computed
+    cache = cls.PagedCache(3, 8, 64, 2, d, bits, n_pages=1)
+    cache.lengths.fill_(40)
+    q = torch.ones(4, 8, d, dtype=torch.float16, device="cuda")
+    cu = torch.tensor([0, 2, 0, 2], dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 3.0)
+    cache.attend(q, cu_seqlens=cu, out=out)
+    assert (out[:2] == 0).all() and (out[2:] == 3).all()
+
+
 # ------------------------------------------------------------------------------- together
 def test_a_run_of_steps_streams_and_graphs(cuda_lib):
     """Prompt, then steps of one token: append + attend on a side stream, captured once and
