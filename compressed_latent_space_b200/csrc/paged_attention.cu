@@ -1067,8 +1067,6 @@ int key_tile_log2(const PagedArgs &a) {
   return a.bits == 16 && a.D >= 64 ? (a.D == 128 ? 4 : 5) : 6;     // Shape::KTL
 }
 
-// CTAs of a launch: as many as the device holds at once by registers and shared memory (227 KB
-// an SM), but no more than the units there can be.
 // Shared memory of a CTA: the rings and the units before each sequence.
 size_t attn_smem(const PagedArgs &a) {
   const int rowb = a.bits == 4 ? a.D / 2 : 2 * a.D, kt = 1 << key_tile_log2(a);
@@ -1083,6 +1081,8 @@ int whole_tiles(const PagedArgs &a) {
   return cap <= 256 ? static_cast<int>((cap + (1 << key_tile_log2(a)) - 1) >> key_tile_log2(a)) : 0;
 }
 
+// CTAs of a launch: as many as the device holds at once by registers and shared memory (227 KB
+// an SM), but no more than the units there can be.
 int plan_ctas(const PagedArgs &a) {
   if (use_tc(a)) return num_sms();
   long long per_sm = (227 * 1024) / static_cast<long long>(attn_smem(a) + 2048);
